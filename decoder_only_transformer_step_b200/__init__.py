@@ -45,6 +45,20 @@ class gpt2_buffers(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class gpt2_decode_opts(ctypes.Structure):
+    _fields_ = [("q4", ctypes.c_void_p), ("q4_bytes", ctypes.c_size_t), ("q4_group", ctypes.c_int),
+                ("prefix", ctypes.c_void_p), ("prefix_bytes", ctypes.c_size_t), ("prefix_cap", ctypes.c_int),
+                ("prefix_len", ctypes.c_int), ("scratch", ctypes.c_void_p), ("scratch_bytes", ctypes.c_size_t)]
+
+
+class gpt2_logit_rules(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_len", ctypes.c_void_p), ("gen_start", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p), ("allowed", ctypes.c_void_p),
+                ("history_ld", ctypes.c_int), ("n_bias", ctypes.c_int), ("allowed_ld", ctypes.c_int),
+                ("append", ctypes.c_int)]
+
+
 EXPORTS = [
     "gpt2_param_count", "gpt2_workspace_bytes", "gpt2_tensor_info", "gpt2_create", "gpt2_destroy",
     "gpt2_init_params", "gpt2_refresh_shadow", "gpt2_forward_loss", "gpt2_backward",
@@ -58,6 +72,10 @@ EXPORTS = [
     "gpt2_op_lm_head_ce_scratch_bytes", "gpt2_op_lm_head_ce_fwd_bf16", "gpt2_op_lm_head_ce_bwd_bf16",
     "gpt2_set_wait_timeout_ns", "gpt2_op_gemm_bf16_status", "gpt2_backward_bucketed",
     "gpt2_op_linear_bf16", "gpt2_graph_capture", "gpt2_graph_step", "gpt2_graph_release",
+    "gpt2_q4_bytes", "gpt2_q4_pack", "gpt2_decode_scratch_bytes", "gpt2_decode_step_ex", "gpt2_rules_next",
+    "gpt2_op_q4_packed_bytes", "gpt2_op_q4_scale_count", "gpt2_op_q4_quantize", "gpt2_op_q4_dequantize",
+    "gpt2_op_gemv_q4", "gpt2_op_prefix_attention_scratch_bytes", "gpt2_op_prefix_attention_bf16",
+    "gpt2_op_logit_rules",
 ]
 
 _LIB = None
@@ -116,6 +134,19 @@ def _lib():
         "gpt2_graph_capture": (I, [P, I, F, I, P, P]),
         "gpt2_graph_step": (I, [P, P, P, P]),
         "gpt2_graph_release": (I, [P]),
+        "gpt2_q4_bytes": (S, [cfgp, I]),
+        "gpt2_q4_pack": (I, [P, P, S, I, P]),
+        "gpt2_decode_scratch_bytes": (S, [cfgp, I, I, I]),
+        "gpt2_decode_step_ex": (I, [P, P, S, I, I, P, P, ctypes.POINTER(gpt2_decode_opts), P, P]),
+        "gpt2_rules_next": (I, [P, P, I, ctypes.POINTER(gpt2_logit_rules), P, P, P]),
+        "gpt2_op_q4_packed_bytes": (S, [I, I]),
+        "gpt2_op_q4_scale_count": (S, [I, I, I]),
+        "gpt2_op_q4_quantize": (I, [P, I, I, I, I, I, P, P, P]),
+        "gpt2_op_q4_dequantize": (I, [P, P, I, I, I, P, I, I, P]),
+        "gpt2_op_gemv_q4": (I, [P, I, P, P, P, P, I, I, I, I, I, I, P]),
+        "gpt2_op_prefix_attention_scratch_bytes": (S, [I, I, I, I, I, I]),
+        "gpt2_op_prefix_attention_bf16": (I, [P, I, P, P, I, I, P, P, P, I, P, I, P, P, S, I, I, I, I, P]),
+        "gpt2_op_logit_rules": (I, [P, I, P, I, I, I, ctypes.POINTER(gpt2_logit_rules), P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -377,6 +408,196 @@ def gpt2_op_gemm_bf16_status(A, a_mn, lda, B, b_mn, ldb, C, c_fp32, ldc, M, N, K
                                            _stream(stream)), "gpt2_op_gemm_bf16_status")
 
 
+# ---- 4-bit weights, shared prefixes, rules on logits ------------------------
+# These calls know every buffer's extent, so they check it here: a buffer that
+# is too short, of another type or on another device is GPT2_ERR_INVALID_ARG
+# instead of a read out of range.
+
+def _buf(where, name, t, dtypes, need, optional=False):
+    """Address of a device buffer of at least `need` elements (counted along a
+    strided view's last element), or None."""
+    import torch
+    if t is None:
+        if optional or need <= 0:
+            return None
+        raise Gpt2Error(-1, f"{where}: {name} is missing")
+    if t.dtype not in dtypes:
+        raise Gpt2Error(-1, f"{where}: {name} is {t.dtype}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise Gpt2Error(-1, f"{where}: {name} is on {t.device}, not on the current CUDA device")
+    have = t.numel()
+    if have < need and have and not t.is_contiguous():
+        have = 1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+    if have < need:
+        raise Gpt2Error(-1, f"{where}: {name} holds {have} elements, {need} are needed")
+    return t.data_ptr()
+
+
+def _cuda_stream(stream):
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _types():
+    import torch
+    global _BF, _F32, _U8, _I32, _W32
+    _BF, _F32, _U8, _I32 = (torch.bfloat16,), (torch.float32,), (torch.uint8,), (torch.int32,)
+    _W32 = (torch.int32, torch.uint32)
+
+
+_BF = _F32 = _U8 = _I32 = _W32 = None
+
+
+def _extent(rows, ld, cols):
+    """Elements from the first of a [rows, cols] matrix of pitch ld to its last."""
+    return (rows - 1) * ld + cols if rows > 0 and cols > 0 else 0
+
+
+def gpt2_op_q4_packed_bytes(N, K) -> int:
+    return int(_lib().gpt2_op_q4_packed_bytes(N, K))
+
+
+def gpt2_op_q4_scale_count(N, K, group) -> int:
+    return int(_lib().gpt2_op_q4_scale_count(N, K, group))
+
+
+def gpt2_op_q4_quantize(w, w_fp32, ldw, N, K, group, packed, scales, stream=None):
+    """w [N, ldw] bf16 (or fp32 with w_fp32) -> packed uint8 [N, K/2], scales bf16 [K/group, N up to a multiple of 8]."""
+    if _BF is None:
+        _types()
+    f = "gpt2_op_q4_quantize"
+    _check(_lib().gpt2_op_q4_quantize(
+        _buf(f, "w", w, _F32 if w_fp32 else _BF, _extent(N, ldw, K)), w_fp32, ldw, N, K, group,
+        _buf(f, "packed", packed, _U8, N * K // 2),
+        _buf(f, "scales", scales, _BF, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), _cuda_stream(stream)), f)
+
+
+def gpt2_op_q4_dequantize(packed, scales, N, K, group, out, out_fp32, ldo, stream=None):
+    if _BF is None:
+        _types()
+    f = "gpt2_op_q4_dequantize"
+    _check(_lib().gpt2_op_q4_dequantize(
+        _buf(f, "packed", packed, _U8, N * K // 2),
+        _buf(f, "scales", scales, _BF, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), N, K, group,
+        _buf(f, "out", out, _F32 if out_fp32 else _BF, _extent(N, ldo, K)), out_fp32, ldo, _cuda_stream(stream)), f)
+
+
+def gpt2_op_gemv_q4(x, ldx, packed, scales, bias, out, out_fp32, ldo, rows, N, K, group, stream=None):
+    """out [rows, ldo] = x [rows, ldx] W^T (+ bias) with W's 4-bit form; rows 1..16."""
+    if _BF is None:
+        _types()
+    f = "gpt2_op_gemv_q4"
+    _check(_lib().gpt2_op_gemv_q4(
+        _buf(f, "x", x, _BF, _extent(rows, ldx, K)), ldx, _buf(f, "packed", packed, _U8, N * K // 2),
+        _buf(f, "scales", scales, _BF, K // group * ((N + 7) // 8 * 8) if group > 0 else 0),
+        _buf(f, "bias", bias, _BF, N, True), _buf(f, "out", out, _F32 if out_fp32 else _BF, _extent(rows, ldo, N)),
+        out_fp32, ldo, rows, N, K, group, _cuda_stream(stream)), f)
+
+
+def gpt2_op_prefix_attention_scratch_bytes(B, Hq, Hkv, hd, prefix_len, max_len) -> int:
+    return int(_lib().gpt2_op_prefix_attention_scratch_bytes(B, Hq, Hkv, hd, prefix_len, max_len))
+
+
+def gpt2_op_prefix_attention_bf16(q, ldq, pk, pv, prefix_len, prefix_cap, k, v, len, max_len, o, ldo, lse, scratch, B, Hq,
+                                  Hkv, hd, stream=None):
+    """One token per row over the shared prefix pk, pv [Hkv, prefix_cap, hd] and the rows' own k, v
+    [B, Hkv, max_len, hd], of which the first prefix_len and len[b] positions count."""
+    if _BF is None:
+        _types()
+    f = "gpt2_op_prefix_attention_bf16"
+    np = _extent(Hkv, prefix_cap * hd, prefix_len * hd)
+    no = B * Hkv * max_len * hd
+    _check(_lib().gpt2_op_prefix_attention_bf16(
+        _buf(f, "q", q, _BF, _extent(B, ldq, Hq * hd)), ldq, _buf(f, "pk", pk, _BF, np), _buf(f, "pv", pv, _BF, np),
+        prefix_len, prefix_cap, _buf(f, "k", k, _BF, no), _buf(f, "v", v, _BF, no),
+        _buf(f, "len", len, _I32, B if max_len > 0 else 0), max_len, _buf(f, "o", o, _BF, _extent(B, ldo, Hq * hd)), ldo,
+        _buf(f, "lse", lse, _F32, B * Hq, True), _buf(f, "scratch", scratch, _U8, 1), scratch.numel(), B, Hq, Hkv, hd,
+        _cuda_stream(stream)), f)
+
+
+class LogitRules:
+    """Rules on the logits of a batch (see gpt2_logit_rules): device tensors,
+    None where a rule is not asked for.  history int32 [rows, capacity] with
+    history_len int32 [rows] and, where the history starts with a prompt,
+    gen_start int32 [rows]; repetition, presence, frequency fp32 [rows];
+    bias_ids int32 and bias_values fp32 [rows, n]; allowed int32 or uint32
+    [rows, words], bit v % 32 of word v // 32 set where id v may be chosen;
+    append: the chosen id is added to the history.  The tensors stay the
+    caller's and are read at every call, so they can be changed in between."""
+
+    def __init__(self, history=None, history_len=None, gen_start=None, repetition=None, presence=None, frequency=None,
+                 bias_ids=None, bias_values=None, allowed=None, append=False):
+        if _BF is None:
+            _types()
+        f = "LogitRules"
+        per_row = dict(history_len=history_len, gen_start=gen_start, repetition=repetition, presence=presence,
+                       frequency=frequency)
+        tables = dict(history=history, bias_ids=bias_ids, bias_values=bias_values, allowed=allowed)
+        rows = {t.shape[0] for t in (*per_row.values(), *tables.values()) if t is not None}
+        for name, t in (*per_row.items(), *tables.items()):
+            if t is not None and (t.dim() != (1 if name in per_row else 2) or not t.is_contiguous()):
+                raise Gpt2Error(-1, f"{f}: {name} has shape {tuple(t.shape)} or is not contiguous")
+        if len(rows) > 1:
+            raise Gpt2Error(-1, f"{f}: the rules are for {sorted(rows)} rows")
+        if (bias_ids is None) != (bias_values is None) or (bias_ids is not None and bias_ids.shape != bias_values.shape):
+            raise Gpt2Error(-1, f"{f}: bias_ids and bias_values belong together")
+        if history is not None and history_len is None:
+            raise Gpt2Error(-1, f"{f}: a history needs history_len")
+        self.rows = rows.pop() if rows else None
+        self.tensors = {**per_row, **tables}
+        width = {n: 0 if t is None else t.shape[1] for n, t in tables.items()}
+        self.c = gpt2_logit_rules(
+            _buf(f, "history", history, _I32, 0), _buf(f, "history_len", history_len, _I32, 0),
+            _buf(f, "gen_start", gen_start, _I32, 0), _buf(f, "repetition", repetition, _F32, 0),
+            _buf(f, "presence", presence, _F32, 0), _buf(f, "frequency", frequency, _F32, 0),
+            _buf(f, "bias_ids", bias_ids, _I32, 0), _buf(f, "bias_values", bias_values, _F32, 0),
+            _buf(f, "allowed", allowed, _W32, 0), width["history"], width["bias_ids"], width["allowed"], int(append))
+        self._ref = ctypes.byref(self.c)
+
+
+def _rules(where, rules, rows):
+    if rules.rows is not None and rules.rows != rows:
+        raise Gpt2Error(-1, f"{where}: rules for {rules.rows} rows, logits of {rows}")
+    return rules._ref
+
+
+def gpt2_op_logit_rules(logits, ld, out, ldo, rows, vocab, rules, next_tokens=None, pos=None, stream=None):
+    """out [rows, ldo] = logits [rows, ld] under `rules` (a LogitRules); next_tokens: the greedy choice."""
+    if _BF is None:
+        _types()
+    f = "gpt2_op_logit_rules"
+    _check(_lib().gpt2_op_logit_rules(
+        _buf(f, "logits", logits, _F32, _extent(rows, ld, vocab)), ld, _buf(f, "out", out, _F32, _extent(rows, ldo, vocab)),
+        ldo, rows, vocab, _rules(f, rules, rows), _buf(f, "next_tokens", next_tokens, _I32, rows, True),
+        _buf(f, "pos", pos, _I32, rows, True), _cuda_stream(stream)), f)
+
+
+def gpt2_rules_next(ctx, logits, batch, rules, next_tokens, pos=None, stream=None):
+    """gpt2_greedy_next under `rules` (a LogitRules); logits are rewritten in place."""
+    _check(_lib().gpt2_rules_next(ctx, _ptr(logits), batch, _rules("gpt2_rules_next", rules, batch), _ptr(next_tokens),
+                                  _ptr(pos), _stream(stream)), "gpt2_rules_next")
+
+
+def gpt2_q4_bytes(cfg: gpt2_config, group: int) -> int:
+    return int(_lib().gpt2_q4_bytes(ctypes.byref(cfg), group))
+
+
+def gpt2_q4_pack(ctx, q4, group, stream=None):
+    """q4: a device uint8 tensor of at least gpt2_q4_bytes(cfg, group) bytes."""
+    _check(_lib().gpt2_q4_pack(ctx, _ptr(q4), _nbytes(q4), group, _stream(stream)), "gpt2_q4_pack")
+
+
+def gpt2_decode_scratch_bytes(cfg: gpt2_config, batch: int, max_len: int, prefix_len: int) -> int:
+    return int(_lib().gpt2_decode_scratch_bytes(ctypes.byref(cfg), batch, max_len, prefix_len))
+
+
+def gpt2_decode_step_ex(ctx, cache, batch, max_len, tokens, pos, opts, logits, stream=None):
+    """gpt2_decode_step with a gpt2_decode_opts (or None)."""
+    _check(_lib().gpt2_decode_step_ex(ctx, _ptr(cache), _nbytes(cache), batch, max_len, _ptr(tokens), _ptr(pos),
+                                      None if opts is None else ctypes.byref(opts), _ptr(logits), _stream(stream)),
+           "gpt2_decode_step_ex")
+
+
 # ------------------------------------------------------------ convenience ---
 
 @dataclass(frozen=True)
@@ -509,28 +730,73 @@ class GPT2:
                        beta2, eps, weight_decay, step)
 
 
+class Q4Weights:
+    """4-bit weights of one GPT2 context for decoding, in groups of ``group``
+    inputs (modes 0 and 2).  ``pack()`` quantises the context's current master
+    weights; call it again after they change."""
+
+    def __init__(self, model: "GPT2", group: int = 64):
+        import torch
+        nbytes = gpt2_q4_bytes(model.cfg, group)
+        if nbytes == 0:
+            raise ValueError(f"no 4-bit form with group={group} for {model.mc}")
+        self.model, self.group = model, group
+        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=model.master.device)
+        self.pack()
+
+    def pack(self):
+        gpt2_q4_pack(self.model.ctx, self.buf, self.group)
+
+
 class KVCache:
     """Key/value cache of one GPT2 context for ``batch`` sequences of up to
     ``max_len`` positions, with the device-side token, position and logits
     buffers a decode loop runs on (so the loop can be captured in a CUDA
-    graph)."""
+    graph).
 
-    def __init__(self, model: "GPT2", batch: int, max_len: int):
+    ``q4``: a Q4Weights whose weights the steps read.  ``prefix``: a KVCache of
+    one sequence, already filled, whose first ``prefix_len`` positions precede
+    every row's own (``prefix_len + max_len <= n_ctx``); the rows' own tokens,
+    prompts included, are then fed by ``step``."""
+
+    def __init__(self, model: "GPT2", batch: int, max_len: int, prefix: "KVCache" = None, prefix_len: int = 0,
+                 q4: Q4Weights = None):
         import torch
         nbytes = gpt2_kv_cache_bytes(model.cfg, batch, max_len)
         if nbytes == 0:
             raise ValueError(f"invalid cache size batch={batch} max_len={max_len}")
+        if q4 is not None and q4.model is not model:
+            raise ValueError("q4 holds the weights of another model")
+        if prefix is not None and (prefix.model is not model or prefix.batch != 1 or prefix.opts_prefix):
+            raise ValueError("a prefix is a KVCache of the same model with one row and no prefix of its own")
+        if prefix is None and prefix_len or not 0 <= prefix_len <= (prefix.max_len if prefix is not None else 0) or \
+                prefix_len + max_len > model.mc.n_ctx:
+            raise ValueError(f"invalid prefix_len {prefix_len}")
         dev = model.master.device
         self.model, self.batch, self.max_len = model, batch, max_len
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self.tokens = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.pos = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.logits = torch.zeros(batch, model.cfg.vocab_padded, dtype=torch.float32, device=dev)
+        self.prefix, self.q4, self.opts = prefix, q4, None
+        self.opts_prefix = prefix is not None and prefix_len > 0
+        if q4 is not None or self.opts_prefix:
+            self.opts = gpt2_decode_opts()
+            if q4 is not None:
+                self.opts.q4, self.opts.q4_bytes, self.opts.q4_group = q4.buf.data_ptr(), _nbytes(q4.buf), q4.group
+            if self.opts_prefix:
+                n = gpt2_decode_scratch_bytes(model.cfg, batch, max_len, prefix_len)
+                self.scratch = torch.empty(n, dtype=torch.uint8, device=dev)
+                self.opts.prefix, self.opts.prefix_bytes = prefix.buf.data_ptr(), _nbytes(prefix.buf)
+                self.opts.prefix_cap, self.opts.prefix_len = prefix.max_len, prefix_len
+                self.opts.scratch, self.opts.scratch_bytes = self.scratch.data_ptr(), n
 
     def prefill(self, tokens, prompt_len):
         """tokens: int32 [batch, n_ctx] (device); prompt_len: int32 [batch]
         (device).  Leaves the logits after each prompt in self.logits, the
         greedy next id in self.tokens and self.pos = prompt_len."""
+        if self.opts_prefix:
+            raise ValueError("rows behind a prefix are fed by step(): prefill would not see the prefix")
         gpt2_prefill(self.model.ctx, self.buf, self.batch, self.max_len, tokens, prompt_len, self.logits)
         self.pos.copy_(prompt_len)
         gpt2_greedy_next(self.model.ctx, self.logits, self.batch, self.tokens)
@@ -539,10 +805,17 @@ class KVCache:
     def step(self, tokens=None, pos=None):
         """One decode step on self.tokens / self.pos (or the given device
         tensors); returns the logits [batch, vocab_padded]."""
-        gpt2_decode_step(self.model.ctx, self.buf, self.batch, self.max_len,
-                         self.tokens if tokens is None else tokens, self.pos if pos is None else pos, self.logits)
+        tokens, pos = self.tokens if tokens is None else tokens, self.pos if pos is None else pos
+        if self.opts is None:
+            gpt2_decode_step(self.model.ctx, self.buf, self.batch, self.max_len, tokens, pos, self.logits)
+        else:
+            gpt2_decode_step_ex(self.model.ctx, self.buf, self.batch, self.max_len, tokens, pos, self.opts, self.logits)
         return self.logits
 
-    def greedy_advance(self):
-        """self.tokens = greedy choice from self.logits; self.pos += 1."""
-        gpt2_greedy_next(self.model.ctx, self.logits, self.batch, self.tokens, self.pos)
+    def greedy_advance(self, rules: LogitRules = None):
+        """self.tokens = greedy choice from self.logits (under `rules`, which
+        rewrite self.logits); self.pos += 1."""
+        if rules is None:
+            gpt2_greedy_next(self.model.ctx, self.logits, self.batch, self.tokens, self.pos)
+        else:
+            gpt2_rules_next(self.model.ctx, self.logits, self.batch, rules, self.tokens, self.pos)

@@ -66,6 +66,15 @@ DEVI float warp_max(float v) {
   return v;
 }
 
+// (value, id) order of the greedy choice: NaN above everything, then larger
+// values, then the lower id.
+DEVI bool greedy_better(float a, int ia, float b, int ib) {
+  const bool na = a != a, nb = b != b;
+  if (na != nb) return na;
+  if (!na && a != b) return a > b;
+  return ia < ib;
+}
+
 // 2^x on the MUFU unit (approximate; subnormal results flush to zero).
 DEVI float ex2_approx(float x) {
   float y;

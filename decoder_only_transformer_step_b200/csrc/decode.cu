@@ -580,11 +580,12 @@ __global__ void __launch_bounds__(GV_WARPS * 32) decode_gemv_mma_kernel(const __
 }
 
 // x[r, :] = wte[tok[r]] + wpe[pos[r]] (fp32); an id outside [0, vocab_real)
-// or a position outside [0, limit) raises its status bit and reads row 0.
+// or a position outside [0, limit) raises its status bit and reads row 0 (of
+// the positions from pos0 on, where a shared prefix ends).
 template <typename T>
 __global__ void embed_decode_kernel(const int32_t* tok, const int32_t* pos,
                                     const T* wte, const T* wpe, float* __restrict__ x,
-                                    int d, int vocab_real, int limit, int* err) {
+                                    int d, int vocab_real, int limit, int pos0, int* err) {
   // wait before letting the step's kernels start: they load weights before
   // their own waits, and a kernel before the step may still be writing them
   pdl_wait();
@@ -600,7 +601,7 @@ __global__ void embed_decode_kernel(const int32_t* tok, const int32_t* pos,
     p = 0;
   }
   for (int k = threadIdx.x; k < d; k += blockDim.x)
-    x[(size_t)r * d + k] = to_f(wte[(size_t)id * d + k]) + to_f(wpe[(size_t)p * d + k]);
+    x[(size_t)r * d + k] = to_f(wte[(size_t)id * d + k]) + to_f(wpe[(size_t)(pos0 + p) * d + k]);
 }
 
 constexpr int AD_WARPS = 8;
@@ -728,15 +729,6 @@ __global__ void __launch_bounds__(AD_WARPS * 32)
       o[(size_t)r * d + h * HD + e] = out * inv;
     }
   }
-}
-
-// (value, id) order of the greedy choice: NaN above everything, then larger
-// values, then the lower id.
-DEVI bool greedy_better(float a, int ia, float b, int ib) {
-  const bool na = a != a, nb = b != b;
-  if (na != nb) return na;
-  if (!na && a != b) return a > b;
-  return ia < ib;
 }
 
 // next[r] = argmax over v < vocab_real of logits[r, v]; pos[r] += 1 if pos.
@@ -1002,13 +994,13 @@ size_t decode_gemv_smem(int f32, int rows, int K) {
 }
 
 int decode_embed(int f32, const int32_t* tok, const int32_t* pos, const void* wte, const void* wpe, float* x,
-                 int rows, int d, int vocab_real, int limit, int* err, cudaStream_t st) {
+                 int rows, int d, int vocab_real, int limit, int pos0, int* err, cudaStream_t st) {
   if (f32)
     CUDA_TRY(launch_k(embed_decode_kernel<float>, rows, 256, 0, st, tok, pos, (const float*)wte,
-                      (const float*)wpe, x, d, vocab_real, limit, err));
+                      (const float*)wpe, x, d, vocab_real, limit, pos0, err));
   else
     CUDA_TRY(launch_k(embed_decode_kernel<bf16>, rows, 256, 0, st, tok, pos, (const bf16*)wte, (const bf16*)wpe,
-                      x, d, vocab_real, limit, err));
+                      x, d, vocab_real, limit, pos0, err));
   LAUNCH_CHECK();
   return GPT2_OK;
 }

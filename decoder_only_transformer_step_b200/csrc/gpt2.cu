@@ -772,6 +772,43 @@ int decode_check(gpt2_ctx* c, void* cache, size_t cache_bytes, int batch, int ma
   return GPT2_OK;
 }
 
+// The 4-bit weights: per layer w_qkv, w_o, w_fc, w_mp, then wte as the LM
+// head, each its nibbles and its scales, padded to 256 bytes.
+struct Q4Mat {
+  uint8_t* packed;
+  uint16_t* scales;
+};
+struct Q4Layout {
+  uint8_t* base = nullptr;
+  size_t off[5][2], layer_bytes = 0, head0 = 0, total = 0;  // off: within a layer; [4]: the head, from head0
+  Q4Mat at(size_t b, int i) const {
+    return {base + b + off[i][0], reinterpret_cast<uint16_t*>(base + b + off[i][1])};
+  }
+  Q4Mat mat(int l, int i) const { return at((size_t)l * layer_bytes, i); }
+  Q4Mat head() const { return at(head0, 4); }
+};
+
+bool q4_layout(const Shape& s, int group, void* buf, Q4Layout* q) {
+  if (s.mode || (group != 32 && group != 64 && group != 128) || s.d % group) return false;
+  q->base = reinterpret_cast<uint8_t*>(buf);
+  const long dims[5][2] = {{3 * s.d, s.d}, {s.d, s.d}, {4 * s.d, s.d}, {s.d, 4 * s.d}, {s.V, s.d}};
+  size_t at = 0;
+  for (int i = 0; i < 5; ++i) {
+    if (i == 4) {
+      q->layer_bytes = at;
+      q->head0 = (size_t)s.L * at;
+      at = 0;
+    }
+    const size_t n = (size_t)dims[i][0], k = (size_t)dims[i][1];
+    q->off[i][0] = at;
+    at += (n * k / 2 + 255) & ~(size_t)255;
+    q->off[i][1] = at;
+    at += (k / group * (size_t)q4_pitch((int)n) * 2 + 255) & ~(size_t)255;
+  }
+  q->total = q->head0 + at;
+  return true;
+}
+
 }  // namespace
 
 size_t gpt2_kv_cache_bytes(const gpt2_config* cfg, int batch, int max_len) {
@@ -783,47 +820,133 @@ size_t gpt2_kv_cache_bytes(const gpt2_config* cfg, int batch, int max_len) {
 
 int gpt2_decode_step(gpt2_ctx* c, void* cache, size_t cache_bytes, int batch, int max_len, const int32_t* tokens,
                      const int32_t* pos, float* logits, void* stream) {
+  return gpt2_decode_step_ex(c, cache, cache_bytes, batch, max_len, tokens, pos, nullptr, logits, stream);
+}
+
+size_t gpt2_q4_bytes(const gpt2_config* cfg, int group) {
+  Shape s;
+  Q4Layout ql;
+  if (!shape_from_cfg(cfg, &s) || !q4_layout(s, group, nullptr, &ql)) return 0;
+  return ql.total;
+}
+
+int gpt2_q4_pack(gpt2_ctx* c, void* q4, size_t q4_bytes, int group, void* stream) {
+  Q4Layout ql;
+  if (!c || !q4 || ((uintptr_t)q4 & 255)) return GPT2_ERR_INVALID_ARG;
+  if (!q4_layout(c->s, group, q4, &ql)) return GPT2_ERR_INVALID_ARG;
+  if (q4_bytes < ql.total) return GPT2_ERR_WORKSPACE;
+  const int mats[4] = {W_QKV, W_O, W_FC, W_MP};
+  for (int l = 0; l < (int)c->s.L; ++l)
+    for (int i = 0; i < 4; ++i) {
+      long r, k;
+      lt_dims(c->s.d, mats[i], &r, &k);
+      const Q4Mat m = ql.mat(l, i);
+      TRY(q4_quantize(c->buf.master + c->off.layer(l, mats[i]), 1, k, (int)r, (int)k, group, m.packed, m.scales,
+                      S(stream)));
+    }
+  const Q4Mat m = ql.head();
+  return q4_quantize(c->buf.master + c->off.wte(), 1, c->s.d, (int)c->s.V, (int)c->s.d, group, m.packed, m.scales,
+                     S(stream));
+}
+
+size_t gpt2_decode_scratch_bytes(const gpt2_config* cfg, int batch, int max_len, int prefix_len) {
+  Shape s;
   DecodeLayout dl;
+  if (!shape_from_cfg(cfg, &s) || !decode_layout(s, batch, max_len, nullptr, &dl)) return 0;
+  if (prefix_len < 1 || (long)prefix_len + max_len > s.T) return 0;
+  return prefix_scratch_bytes(batch, (int)s.H, (int)s.H, (int)s.hd, prefix_len, max_len);
+}
+
+int gpt2_decode_step_ex(gpt2_ctx* c, void* cache, size_t cache_bytes, int batch, int max_len, const int32_t* tokens,
+                        const int32_t* pos, const gpt2_decode_opts* opts, float* logits, void* stream) {
+  DecodeLayout dl, pl;
   TRY(decode_check(c, cache, cache_bytes, batch, max_len, &dl));
   if (!tokens || !pos || !logits) return GPT2_ERR_INVALID_ARG;
   const Shape& s = c->s;
   const Offsets& o = c->off;
   const int f32 = s.mode, d = (int)s.d;
   cudaStream_t st = S(stream);
-  TRY(decode_embed(f32, tokens, pos, Wp(c, o.wte()), Wp(c, o.wpe()), dl.x, batch, d, (int)s.Vr, max_len, c->w.err,
+  Q4Layout ql;
+  const bool q4 = opts && opts->q4;
+  if (q4) {
+    if (((uintptr_t)opts->q4 & 255) || !q4_layout(s, opts->q4_group, const_cast<void*>(opts->q4), &ql))
+      return GPT2_ERR_INVALID_ARG;
+    if (opts->q4_bytes < ql.total) return GPT2_ERR_WORKSPACE;
+  }
+  const int P = opts && opts->prefix ? opts->prefix_len : 0;
+  if (opts && opts->prefix) {
+    if (((uintptr_t)opts->prefix & 255) || P < 0 || P > opts->prefix_cap || (long)P + max_len > s.T ||
+        !decode_layout(s, 1, opts->prefix_cap, const_cast<void*>(opts->prefix), &pl) || pl.total > opts->prefix_bytes)
+      return GPT2_ERR_INVALID_ARG;
+    if (P && !f32) {
+      if (!opts->scratch || ((uintptr_t)opts->scratch & 255)) return GPT2_ERR_INVALID_ARG;
+      if (opts->scratch_bytes < prefix_scratch_bytes(batch, (int)s.H, (int)s.H, (int)s.hd, P, max_len))
+        return GPT2_ERR_WORKSPACE;
+    }
+  }
+  TRY(decode_embed(f32, tokens, pos, Wp(c, o.wte()), Wp(c, o.wpe()), dl.x, batch, d, (int)s.Vr, max_len, P, c->w.err,
                    st));
   DecodeGemv g;
   memset(&g, 0, sizeof(g));
   g.rows = batch;
   g.pos = pos;
   g.d = d; g.H = (int)s.H; g.hd = (int)s.hd; g.max_len = max_len;
+  // matrix i of layer l (w_qkv, w_o, w_fc, w_mp; l = -1: the LM head)
+  auto gemv = [&](int l, int i) {
+    if (!q4) return decode_gemv(f32, g, st);
+    const Q4Mat m = l < 0 ? ql.head() : ql.mat(l, i);
+    return decode_gemv_q4(g, m.packed, m.scales, opts->q4_group, st);
+  };
   for (int l = 0; l < (int)s.L; ++l) {
     // LN1 -> QKV (+ bias): q to dl.q, k and v into the cache at pos
     g.in = dl.x; g.in_t = 0; g.W = Wp(c, o.layer(l, W_QKV)); g.bias = Wp(c, o.layer(l, B_QKV));
     g.ln = 1; g.ln_g = Wp(c, o.layer(l, LN1_G)); g.ln_b = Wp(c, o.layer(l, LN1_B));
     g.epi = DECODE_QKV; g.out = dl.q; g.ldo = d; g.N = 3 * d; g.K = d;
     g.kc = dl.k(l); g.vc = dl.v(l);
-    TRY(decode_gemv(f32, g, st));
-    TRY(decode_attention(f32, dl.k(l), dl.v(l), dl.q, dl.o, pos, batch, (int)s.H, (int)s.hd, max_len, st));
+    TRY(gemv(l, 0));
+    int o_bf16 = 0;
+    if (!P) {
+      TRY(decode_attention(f32, dl.k(l), dl.v(l), dl.q, dl.o, pos, batch, (int)s.H, (int)s.hd, max_len, st));
+    } else if (f32) {
+      TRY(prefix_attention_f32(dl.q, (const float*)pl.k(l), (const float*)pl.v(l), P, opts->prefix_cap,
+                               (const float*)dl.k(l), (const float*)dl.v(l), pos, 1, max_len, batch, (int)s.H, (int)s.hd,
+                               dl.o, st));
+    } else {
+      PrefixAttn pa = {};
+      pa.q = dl.q; pa.ldq = d; pa.q_f32 = 1;
+      pa.pk = pl.k(l); pa.pv = pl.v(l); pa.P = P; pa.pcap = opts->prefix_cap;
+      pa.k = dl.k(l); pa.v = dl.v(l); pa.len = pos; pa.len_add = 1; pa.max_len = max_len;
+      pa.o = dl.o; pa.ldo = d;
+      pa.scratch = opts->scratch; pa.scratch_bytes = opts->scratch_bytes;
+      pa.B = batch; pa.Hq = pa.Hkv = (int)s.H; pa.hd = (int)s.hd;
+      TRY(prefix_attention(pa, st));
+      o_bf16 = 1;
+    }
     // x += o W_o^T + b_o
-    g.in = dl.o; g.in_t = 0; g.W = Wp(c, o.layer(l, W_O)); g.bias = Wp(c, o.layer(l, B_O));
+    g.in = dl.o; g.in_t = o_bf16; g.W = Wp(c, o.layer(l, W_O)); g.bias = Wp(c, o.layer(l, B_O));
     g.ln = 0; g.epi = DECODE_RESID; g.out = dl.x; g.ldo = d; g.N = d; g.K = d;
-    TRY(decode_gemv(f32, g, st));
+    TRY(gemv(l, 1));
     // LN2 -> fc (+ bias) -> GELU
     g.in = dl.x; g.in_t = 0; g.W = Wp(c, o.layer(l, W_FC)); g.bias = Wp(c, o.layer(l, B_FC));
     g.ln = 1; g.ln_g = Wp(c, o.layer(l, LN2_G)); g.ln_b = Wp(c, o.layer(l, LN2_B));
     g.epi = DECODE_GELU; g.out = dl.g; g.ldo = 4 * d; g.N = 4 * d; g.K = d;  // GELU(u) in the compute dtype
-    TRY(decode_gemv(f32, g, st));
+    TRY(gemv(l, 2));
     // x += g W_mp^T + b_mp
     g.in = dl.g; g.in_t = 1; g.W = Wp(c, o.layer(l, W_MP)); g.bias = Wp(c, o.layer(l, B_MP));
     g.ln = 0; g.epi = DECODE_RESID; g.out = dl.x; g.ldo = d; g.N = d; g.K = 4 * d;
-    TRY(decode_gemv(f32, g, st));
+    TRY(gemv(l, 3));
   }
   // final LN -> tied LM head
   g.in = dl.x; g.in_t = 0; g.W = Wp(c, o.wte()); g.bias = nullptr;
   g.ln = 1; g.ln_g = Wp(c, o.lnf_g()); g.ln_b = Wp(c, o.lnf_b());
   g.epi = DECODE_LOGITS; g.out = logits; g.ldo = s.V; g.N = (int)s.V; g.K = d;
-  return decode_gemv(f32, g, st);
+  return gemv(-1, 0);
+}
+
+int gpt2_rules_next(gpt2_ctx* c, float* logits, int batch, const gpt2_logit_rules* rules, int32_t* next_tokens,
+                    int32_t* pos, void* stream) {
+  if (!c || !logits || !rules || !next_tokens || batch < 1) return GPT2_ERR_INVALID_ARG;
+  return logit_rules(logits, c->s.V, logits, c->s.V, batch, (int)c->s.Vr, rules, next_tokens, pos, S(stream));
 }
 
 int gpt2_prefill(gpt2_ctx* c, void* cache, size_t cache_bytes, int batch, int max_len, const int32_t* tokens,

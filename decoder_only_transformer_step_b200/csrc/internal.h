@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/gpt2.h"
+
 // Epilogue applied to each GEMM output element (row m, column n, fp32 acc).
 // "act" is the activation type of the mode (bf16 or fp32).
 enum EpiKind : int {
@@ -184,7 +186,7 @@ struct DecodeGemv {
 size_t decode_gemv_smem(int f32, int rows, int K);
 int decode_gemv(int f32, const DecodeGemv& g, cudaStream_t st);
 int decode_embed(int f32, const int32_t* tok, const int32_t* pos, const void* wte, const void* wpe, float* x,
-                 int rows, int d, int vocab_real, int limit, int* err, cudaStream_t st);
+                 int rows, int d, int vocab_real, int limit, int pos0, int* err, cudaStream_t st);
 int decode_attention(int f32, const void* kc, const void* vc, const float* q, float* o, const int32_t* pos,
                      int rows, int H, int hd, int max_len, cudaStream_t st);
 // part_v / part_i: GREEDY_SPLIT_MAX_ROWS x 16 scratch (may be NULL: one block per row)
@@ -195,3 +197,41 @@ int prefill_kv(int f32, const void* qkv, void* kc, void* vc, const int32_t* plen
                int max_len, int limit, int* err, cudaStream_t st);
 int prefill_logits(int f32, const void* logits, const int32_t* plen, float* out, int rows, int T, int V, int limit,
                    cudaStream_t st);
+
+// ---- 4-bit weights with group scales ------------------------------------
+// Nibbles [N, K / 2] and bf16 scales [K / group][q4_pitch(N)] of a weight
+// matrix [N, K]; group 32, 64 or 128, dividing K.
+long q4_pitch(int N);
+int q4_quantize(const void* w, int w_f32, long ldw, int N, int K, int group, uint8_t* packed, uint16_t* scales,
+                cudaStream_t st);
+// decode_gemv (bf16 mode) with such weights in place of g.W.
+int decode_gemv_q4(const DecodeGemv& g, const uint8_t* packed, const uint16_t* scales, int group, cudaStream_t st);
+
+// ---- attention over a shared prefix and each row's own positions ---------
+struct PrefixAttn {
+  const void* q;  // [B, ldq]: bf16, or fp32 (rounded to bf16) where q_f32
+  long ldq;
+  int q_f32;
+  const void *pk, *pv;  // bf16 [Hkv][pcap][hd], the first P positions of each
+  int P;
+  long pcap;
+  const void *k, *v;    // bf16 [B][Hkv][max_len][hd], the first len[b] + len_add of each
+  const int32_t* len;
+  int len_add, max_len;
+  void* o;              // bf16 [B, ldo]
+  long ldo;
+  float* lse;           // [B, Hq] or NULL
+  void* scratch;
+  size_t scratch_bytes;
+  int B, Hq, Hkv, hd;
+};
+size_t prefix_scratch_bytes(int B, int Hq, int Hkv, int hd, int P, int max_len);
+int prefix_attention(const PrefixAttn& c, cudaStream_t st);
+// fp32 form (one head layout: Hq = Hkv = H; q, o [B, H hd])
+int prefix_attention_f32(const float* q, const float* pk, const float* pv, int P, long pcap, const float* k,
+                         const float* v, const int32_t* len, int len_add, int max_len, int B, int H, int hd, float* o,
+                         cudaStream_t st);
+
+// ---- rules on logits (see gpt2_op_logit_rules) ----------------------------
+int logit_rules(const float* logits, long ld, float* out, long ldo, int rows, int vocab, const gpt2_logit_rules* r,
+                int32_t* next, int32_t* pos, cudaStream_t st);

@@ -1,0 +1,548 @@
+// Attention of one new token per sequence over a prefix that the whole batch
+// shares and each sequence's own cached positions behind it.
+//
+//   z[j] = q . k[j] / sqrt(hd),  j over the P prefix keys and the row's own
+//   o = sum_j exp(z[j] - lse) v[j],  lse = log sum_j exp(z[j])
+//
+// The prefix is read once for all rows: the query rows of a key/value head
+// (batch x heads that share it) are the rows of one matrix product per block
+// of keys, instead of B passes over the same keys.  Work is split along the
+// keys into parts of a fixed length; a part leaves, per row, its running
+// maximum, sum and weighted values (fp32), and a second kernel joins a row's
+// parts in a fixed order.  Rows without any key get o = 0, lse = -inf.
+#include "common.cuh"
+#include "internal.h"
+
+namespace {
+
+constexpr int PA_WARPS = 4;      // warps of a block: they share its part's keys
+constexpr int PA_KEYS = 32;      // keys of a warp's step
+constexpr int PA_STAGES = 3;     // steps in a warp's ring
+constexpr int PA_ROWS = 16;      // query rows of a block (the mma M)
+constexpr int PA_BLOCKS = 296;   // blocks a call is spread over: 2 for each of 148 SMs
+constexpr int PA_MIN_PART = PA_WARPS * PA_KEYS;
+
+struct PrefixArgs {
+  const void* q;  // [B, ldq], bf16 or fp32 (rounded to bf16 on load)
+  long ldq;
+  const bf16 *pk, *pv;  // [Hkv][pcap][hd]
+  int P;
+  long pcap;
+  const bf16 *k, *v;  // [B][Hkv][max_len][hd]
+  const int32_t* len;
+  int len_add, max_len;
+  int B, Hq, Hkv, G;
+  float scale_log2;
+  int L;              // keys of a part
+  int nsp, nso;       // parts of the prefix, parts of a row's own keys (at most)
+  int mtp, mto;       // 16-row tiles of a key/value head's rows in the prefix / of its group
+  float* po;          // [nsp + nso][B * Hq][hd]
+  float2* pml;        // [nsp + nso][B * Hq]: maximum (log2 units), sum
+};
+
+DEVI int own_len(const PrefixArgs& a, int b) {
+  if (a.max_len == 0) return 0;  // len may be NULL
+  const int n = a.len[b] + a.len_add;
+  return n < 0 ? 0 : (n > a.max_len ? a.max_len : n);
+}
+
+DEVI void cp_async16z(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;  // 0: the 16 bytes are zeroed, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+DEVI void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+DEVI void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+DEVI void pa_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <typename QT> DEVI uint32_t ld_q2(const QT* p);
+template <> DEVI uint32_t ld_q2<bf16>(const bf16* p) { return *reinterpret_cast<const uint32_t*>(p); }
+template <> DEVI uint32_t ld_q2<float>(const float* p) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  return pack_bf16x2(v.x, v.y);
+}
+
+template <int HD> constexpr int pa_smem() { return PA_WARPS * PA_STAGES * 2 * PA_KEYS * HD * 2; }
+
+// One part of the keys for up to 16 query rows.  Bound by HBM reads of keys
+// and values: 4 hd bytes a key feed 16 rows' products (mma.sync m16n8k16),
+// which take a few percent of the tensor cores' time, so each warp streams
+// its own steps of 32 keys through a ring of its own (cp.async, two steps
+// ahead) without block-wide waits, with its own running maximum and sum; the
+// warps meet once at the end.  Probabilities are rounded to bf16 for the
+// second product (its operand type; their sum stays fp32 of the unrounded
+// ones): half a step, 2^-8 relative at most, as the output's own rounding.
+template <int HD, typename QT>
+__global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid_constant__ PrefixArgs a) {
+  extern __shared__ __align__(128) uint8_t pa_smem_buf[];
+  constexpr int C = HD / 8;                       // 16-byte chunks of a key
+  constexpr int SWZ = C < 8 ? C - 1 : 7;          // chunk index ^ (key & SWZ): ldmatrix rows in distinct banks
+  constexpr int KB = PA_KEYS * HD * 2;            // bytes of a step's keys (and of its values)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  pdl_trigger();
+  pdl_wait();
+  // which part: those of the prefix first (the tiles of one key range next to
+  // each other, for L2), then the rows' own
+  const int np = a.nsp * a.Hkv * a.mtp;
+  int x = blockIdx.x, part, h, mt, b0 = 0, n, nrows;
+  const bf16 *kb, *vb;
+  const bool shared_keys = x < np;
+  if (shared_keys) {
+    mt = x % a.mtp;
+    h = x / a.mtp % a.Hkv;
+    part = x / (a.mtp * a.Hkv);
+    n = a.P;
+    kb = a.pk + (size_t)h * a.pcap * HD;
+    vb = a.pv + (size_t)h * a.pcap * HD;
+    nrows = a.B * a.G;
+  } else {
+    x -= np;
+    mt = x % a.mto;
+    h = x / a.mto % a.Hkv;
+    b0 = x / (a.mto * a.Hkv) % a.B;
+    part = x / (a.mto * a.Hkv * a.B);
+    n = own_len(a, b0);
+    kb = a.k + ((size_t)b0 * a.Hkv + h) * a.max_len * HD;
+    vb = a.v + ((size_t)b0 * a.Hkv + h) * a.max_len * HD;
+    nrows = a.G;
+  }
+  const int k0 = part * a.L, k1 = min(n, k0 + a.L);
+  if (k0 >= k1) return;
+  // row i of the tile -> (sequence, query head)
+  auto row_of = [&](int i, int* b, int* hq) {
+    const int m = mt * PA_ROWS + i;
+    *b = shared_keys ? m / a.G : b0;
+    *hq = h * a.G + (shared_keys ? m % a.G : m);
+    return m < nrows;
+  };
+  const uint32_t ring = smem_u32(pa_smem_buf) + warp * (PA_STAGES * 2 * KB);
+  const int nsteps = (k1 - k0 + PA_KEYS - 1) / PA_KEYS;
+  int ps = warp, pslot = 0;
+  auto issue = [&]() {
+    if (ps < nsteps) {
+      const int j0 = k0 + ps * PA_KEYS;
+      const uint32_t dst = ring + pslot * 2 * KB;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int e = lane + 32 * i, key = e / C, ch = e % C;
+        const bool live = j0 + key < k1;
+        const size_t at = (size_t)(live ? j0 + key : k0) * HD + ch * 8;
+        const uint32_t d = dst + key * (HD * 2) + ((ch ^ (key & SWZ)) << 4);
+        cp_async16z(d, kb + at, live);
+        cp_async16z(d + KB, vb + at, live);
+      }
+      ps += PA_WARPS;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    pslot = pslot + 1 == PA_STAGES ? 0 : pslot + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < PA_STAGES - 1; ++i) issue();
+
+  uint32_t qf[HD / 16][4];
+  {
+    int ba, ha, bb, hb;
+    const bool la = row_of(g, &ba, &ha), lb = row_of(g + 8, &bb, &hb);
+    const QT* qa = reinterpret_cast<const QT*>(a.q) + (la ? (size_t)ba * a.ldq + ha * HD : 0) + 2 * t;
+    const QT* qb = reinterpret_cast<const QT*>(a.q) + (lb ? (size_t)bb * a.ldq + hb * HD : 0) + 2 * t;
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) {
+      qf[c][0] = la ? ld_q2<QT>(qa + 16 * c) : 0u;
+      qf[c][1] = lb ? ld_q2<QT>(qb + 16 * c) : 0u;
+      qf[c][2] = la ? ld_q2<QT>(qa + 16 * c + 8) : 0u;
+      qf[c][3] = lb ? ld_q2<QT>(qb + 16 * c + 8) : 0u;
+    }
+  }
+  // running maximum (in log2 units of the scaled scores), sum, values
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, o[HD / 8][4];
+#pragma unroll
+  for (int i = 0; i < HD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  // ldmatrix addresses: K as 8x8 (keys, dims) tiles, V transposed
+  const int kkey = ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
+  const int vkey = (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
+  int cslot = 0;
+  for (int s = warp; s < nsteps; s += PA_WARPS) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PA_STAGES - 2) : "memory");
+    __syncwarp();
+    issue();
+    const uint32_t kt = ring + cslot * 2 * KB, vt = kt + KB;
+    float z[PA_KEYS / 8][4];
+#pragma unroll
+    for (int i = 0; i < PA_KEYS / 8; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) {
+#pragma unroll
+      for (int j = 0; j < PA_KEYS / 16; ++j) {
+        uint32_t r[4];
+        const int key = 16 * j + kkey;
+        ldsm4(kt + key * (HD * 2) + (((2 * c + kch) ^ (key & SWZ)) << 4), r);
+        pa_mma(z[2 * j], qf[c], r[0], r[1]);
+        pa_mma(z[2 * j + 1], qf[c], r[2], r[3]);
+      }
+    }
+    const int left = k1 - (k0 + s * PA_KEYS);
+    if (left < PA_KEYS) {
+#pragma unroll
+      for (int i = 0; i < PA_KEYS / 8; ++i) {
+        const int key = 8 * i + 2 * t;
+        if (key >= left) z[i][0] = z[i][2] = -INFINITY;
+        if (key + 1 >= left) z[i][1] = z[i][3] = -INFINITY;
+      }
+    }
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PA_KEYS / 8; ++i) {
+      x0 = fmaxf(x0, fmaxf(z[i][0], z[i][1]));
+      x1 = fmaxf(x1, fmaxf(z[i][2], z[i][3]));
+    }
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+    x0 *= a.scale_log2;
+    x1 *= a.scale_log2;
+    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+      const float y0 = fmaxf(m0, x0), y1 = fmaxf(m1, x1);
+      const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - y0), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - y1);
+      m0 = y0;
+      m1 = y1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) {
+        o[i][0] *= f0;
+        o[i][1] *= f0;
+        o[i][2] *= f1;
+        o[i][3] *= f1;
+      }
+    }
+    const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+    for (int i = 0; i < PA_KEYS / 8; ++i) {
+      z[i][0] = ex2_approx(fmaf(z[i][0], a.scale_log2, -r0));
+      z[i][1] = ex2_approx(fmaf(z[i][1], a.scale_log2, -r0));
+      z[i][2] = ex2_approx(fmaf(z[i][2], a.scale_log2, -r1));
+      z[i][3] = ex2_approx(fmaf(z[i][3], a.scale_log2, -r1));
+      l0 += z[i][0] + z[i][1];
+      l1 += z[i][2] + z[i][3];
+    }
+#pragma unroll
+    for (int j = 0; j < PA_KEYS / 16; ++j) {
+      const uint32_t p[4] = {pack_bf16x2(z[2 * j][0], z[2 * j][1]), pack_bf16x2(z[2 * j][2], z[2 * j][3]),
+                             pack_bf16x2(z[2 * j + 1][0], z[2 * j + 1][1]), pack_bf16x2(z[2 * j + 1][2], z[2 * j + 1][3])};
+      const int key = 16 * j + vkey;
+#pragma unroll
+      for (int c = 0; c < HD / 16; ++c) {
+        uint32_t r[4];
+        ldsm4t(vt + key * (HD * 2) + (((2 * c + vch) ^ (key & SWZ)) << 4), r);
+        pa_mma(o[2 * c], p, r[0], r[1]);
+        pa_mma(o[2 * c + 1], p, r[2], r[3]);
+      }
+    }
+    cslot = cslot + 1 == PA_STAGES ? 0 : cslot + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  // the warps' sums meet in shared memory (over the rings, all of whose
+  // copies have landed): [warp][16][HD + 4] values, [warp][16] (maximum, sum)
+  __syncthreads();
+  constexpr int OP = HD + 4;
+  float* so = reinterpret_cast<float*>(pa_smem_buf);
+  float2* sml = reinterpret_cast<float2*>(so + PA_WARPS * PA_ROWS * OP);
+#pragma unroll
+  for (int i = 0; i < HD / 8; ++i) {
+    float* d = so + (warp * PA_ROWS + g) * OP + 8 * i + 2 * t;
+    *reinterpret_cast<float2*>(d) = make_float2(o[i][0], o[i][1]);
+    *reinterpret_cast<float2*>(d + 8 * OP) = make_float2(o[i][2], o[i][3]);
+  }
+  if (t == 0) {
+    sml[warp * PA_ROWS + g] = make_float2(m0, l0);
+    sml[warp * PA_ROWS + g + 8] = make_float2(m1, l1);
+  }
+  __syncthreads();
+  const int slot = shared_keys ? part : a.nsp + part;
+  for (int i = threadIdx.x; i < PA_ROWS * (HD / 4); i += PA_WARPS * 32) {
+    const int row = i / (HD / 4), c = i % (HD / 4) * 4;
+    int b, hq;
+    if (!row_of(row, &b, &hq)) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < PA_WARPS; ++w) M = fmaxf(M, sml[w * PA_ROWS + row].x);
+    float lsum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < PA_WARPS; ++w) {
+      const float2 ml = sml[w * PA_ROWS + row];
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      const float4 ow = *reinterpret_cast<const float4*>(so + (w * PA_ROWS + row) * OP + c);
+      lsum = fmaf(f, ml.y, lsum);
+      v.x = fmaf(f, ow.x, v.x);
+      v.y = fmaf(f, ow.y, v.y);
+      v.z = fmaf(f, ow.z, v.z);
+      v.w = fmaf(f, ow.w, v.w);
+    }
+    const size_t at = (size_t)slot * a.B * a.Hq + (size_t)b * a.Hq + hq;
+    *reinterpret_cast<float4*>(a.po + at * HD + c) = v;
+    if (c == 0) a.pml[at] = make_float2(M, lsum);
+  }
+}
+
+// Joins the parts of a row (in the order of the parts): a block a row, its
+// warps take the parts in turn, a lane the same dims of each.
+template <int HD>
+__global__ void __launch_bounds__(128)
+    prefix_join_kernel(const __grid_constant__ PrefixArgs a, bf16* __restrict__ o, long ldo, float* __restrict__ lse) {
+  constexpr int V = HD >= 128 ? 4 : 2;   // dims of a lane
+  constexpr int NL = HD / V;             // lanes at work (8 at hd 16)
+  constexpr int U = 4;                   // parts in flight
+  __shared__ float so[4][HD];
+  __shared__ float2 sml[4];
+  pdl_start();
+  const int row = blockIdx.x, b = row / a.Hq, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nown = (own_len(a, b) + a.L - 1) / a.L, n = a.nsp + nown;  // the row's parts: slots 0 .. n - 1
+  const size_t rows = (size_t)a.B * a.Hq;
+  float M = -INFINITY, l = 0.f, acc[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int p0 = warp; p0 < n; p0 += 4 * U) {
+    float2 ml[U];
+    float v[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + 4 * u;
+      ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[u][e] = 0.f;
+      if (p < n) {
+        const size_t at = (size_t)p * rows + row;
+        ml[u] = a.pml[at];
+        if (lane < NL) {
+          const float* src = a.po + at * HD + lane * V;
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const float2 w = *reinterpret_cast<const float2*>(src + e);
+            v[u][e] = w.x;
+            v[u][e + 1] = w.y;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (p0 + 4 * u >= n) break;
+      const float Mn = fmaxf(M, ml[u].x);
+      const float fa = M == -INFINITY ? 0.f : ex2_approx(M - Mn), fb = ml[u].x == -INFINITY ? 0.f : ex2_approx(ml[u].x - Mn);
+      M = Mn;
+      l = l * fa + ml[u].y * fb;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = acc[e] * fa + v[u][e] * fb;
+    }
+  }
+  if (lane < NL)
+#pragma unroll
+    for (int e = 0; e < V; ++e) so[warp][lane * V + e] = acc[e];
+  if (lane == 0) sml[warp] = make_float2(M, l);
+  __syncthreads();
+  float T = -INFINITY, L = 0.f, f[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) T = fmaxf(T, sml[w].x);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = sml[w].x == -INFINITY ? 0.f : ex2_approx(sml[w].x - T);
+    L = fmaf(f[w], sml[w].y, L);
+  }
+  const float inv = n > 0 ? 1.f / L : 0.f;
+  if (threadIdx.x < HD / 2) {
+    const int e = 2 * threadIdx.x;
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      x = fmaf(f[w], so[w][e], x);
+      y = fmaf(f[w], so[w][e + 1], y);
+    }
+    *reinterpret_cast<uint32_t*>(o + (size_t)b * ldo + (size_t)(row % a.Hq) * HD + e) = pack_bf16x2(x * inv, y * inv);
+  }
+  if (lse && threadIdx.x == 0) lse[row] = n > 0 ? fmaf(T, 0.6931471805599453f, logf(L)) : -INFINITY;
+}
+
+// The correctness mode's form, all fp32 on CUDA cores: one warp a (row, head),
+// a lane HD / 32 dims (at hd 16 half the lanes), keys one by one.
+template <int HD>
+__global__ void __launch_bounds__(32)
+    prefix_f32_kernel(const float* q, const float* pk, const float* pv, int P, long pcap, const float* k, const float* v,
+                      const int32_t* len, int len_add, int max_len, int H, float scale, float* __restrict__ o) {
+  constexpr int V = HD >= 32 ? HD / 32 : 1;
+  pdl_start();
+  const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x, d = H * HD;
+  int n = len[b] + len_add;
+  n = n < 0 ? 0 : (n > max_len ? max_len : n);
+  float qv[V], acc[V], m = -INFINITY, l = 0.f;
+  const bool live = lane * V < HD;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    qv[e] = live ? q[(size_t)b * d + h * HD + lane * V + e] * scale : 0.f;
+    acc[e] = 0.f;
+  }
+  for (int j = 0; j < P + n; ++j) {
+    const size_t at = j < P ? ((size_t)h * pcap + j) * HD : (((size_t)b * H + h) * max_len + (j - P)) * HD;
+    const float *kr = (j < P ? pk : k) + at, *vr = (j < P ? pv : v) + at;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (live) s = fmaf(qv[e], kr[lane * V + e], s);
+    s = warp_sum(s);
+    const float mn = fmaxf(m, s), fa = m == -INFINITY ? 0.f : expf(m - mn), p = expf(s - mn);
+    m = mn;
+    l = l * fa + p;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (live) acc[e] = acc[e] * fa + p * vr[lane * V + e];
+  }
+  const float inv = P + n > 0 ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (live) o[(size_t)b * d + h * HD + lane * V + e] = acc[e] * inv;
+}
+
+// The split of a call: parts of L keys, so that about PA_BLOCKS blocks share
+// the keys (the rows' own counted at max_len).  From the sizes alone, not the
+// device: the scratch a caller sizes without one is the scratch a call uses.
+struct PrefixPlan {
+  int L, nsp, nso, mtp, mto;
+  size_t rows, po_bytes, bytes;
+};
+bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan* p) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || P < 0 || max_len < 0) return false;
+  if (hd != 16 && hd != 64 && hd != 128) return false;
+  const int G = Hq / Hkv;
+  p->mtp = (int)(((long)B * G + PA_ROWS - 1) / PA_ROWS);
+  p->mto = (G + PA_ROWS - 1) / PA_ROWS;
+  const double keys = (double)Hkv * p->mtp * P + (double)B * Hkv * p->mto * max_len;
+  long L = (long)(keys / PA_BLOCKS) + 1;
+  L = (L + PA_MIN_PART - 1) / PA_MIN_PART * PA_MIN_PART;
+  const long longest = P > max_len ? P : max_len;
+  if (L > longest + PA_MIN_PART) L = (longest + PA_MIN_PART) / PA_MIN_PART * PA_MIN_PART;
+  p->L = (int)L;
+  p->nsp = (int)((P + L - 1) / L);
+  p->nso = (int)((max_len + L - 1) / L);
+  p->rows = (size_t)B * Hq;
+  p->po_bytes = ((size_t)(p->nsp + p->nso) * p->rows * hd * 4 + 255) & ~(size_t)255;
+  p->bytes = p->po_bytes + (((size_t)(p->nsp + p->nso) * p->rows * 8 + 255) & ~(size_t)255);
+  if (p->bytes == 0) p->bytes = 256;
+  return true;
+}
+
+template <int HD, typename QT>
+int prefix_run(const PrefixArgs& a, bf16* o, long ldo, float* lse, cudaStream_t st) {
+  const long blocks = (long)a.nsp * a.Hkv * a.mtp + (long)a.nso * a.B * a.Hkv * a.mto;
+  if (blocks > 0x7fffffffl || (long)a.B * a.Hq > 0x7fffffffl) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  if (blocks) {
+    CUDA_TRY(once_per_device((const void*)prefix_part_kernel<HD, QT>, [](int) {
+      return cudaFuncSetAttribute(prefix_part_kernel<HD, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  pa_smem<HD>() > 49152 ? pa_smem<HD>() : 49152);
+    }));
+    constexpr int merge = PA_WARPS * PA_ROWS * ((HD + 4) * 4 + 8);
+    CUDA_TRY(launch_k(prefix_part_kernel<HD, QT>, dim3((unsigned)blocks), PA_WARPS * 32,
+                      (size_t)(pa_smem<HD>() > merge ? pa_smem<HD>() : merge), st, a));
+    LAUNCH_CHECK();
+  }
+  CUDA_TRY(launch_k(prefix_join_kernel<HD>, dim3((unsigned)(a.B * a.Hq)), 128, 0, st, a, o, ldo, lse));
+  LAUNCH_CHECK();
+  return GPT2_OK;
+}
+
+}  // namespace
+
+size_t prefix_scratch_bytes(int B, int Hq, int Hkv, int hd, int P, int max_len) {
+  PrefixPlan p;
+  return prefix_plan(B, Hq, Hkv, hd, P, max_len, &p) ? p.bytes : 0;
+}
+
+int prefix_attention(const PrefixAttn& c, cudaStream_t st) {
+  PrefixPlan p;
+  if (!prefix_plan(c.B, c.Hq, c.Hkv, c.hd, c.P, c.max_len, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  if (c.scratch_bytes < p.bytes) return GPT2_ERR_WORKSPACE;
+  PrefixArgs a = {};
+  a.q = c.q; a.ldq = c.ldq;
+  a.pk = reinterpret_cast<const bf16*>(c.pk); a.pv = reinterpret_cast<const bf16*>(c.pv);
+  a.P = c.P; a.pcap = c.pcap;
+  a.k = reinterpret_cast<const bf16*>(c.k); a.v = reinterpret_cast<const bf16*>(c.v);
+  a.len = c.len; a.len_add = c.len_add; a.max_len = c.max_len;
+  a.B = c.B; a.Hq = c.Hq; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv;
+  a.scale_log2 = 1.4426950408889634f / sqrtf((float)c.hd);
+  a.L = p.L; a.nsp = p.nsp; a.nso = p.nso; a.mtp = p.mtp; a.mto = p.mto;
+  a.po = reinterpret_cast<float*>(c.scratch);
+  a.pml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(c.scratch) + p.po_bytes);
+  bf16* o = reinterpret_cast<bf16*>(c.o);
+  if (c.hd == 16)
+    return c.q_f32 ? prefix_run<16, float>(a, o, c.ldo, c.lse, st) : prefix_run<16, bf16>(a, o, c.ldo, c.lse, st);
+  if (c.hd == 64)
+    return c.q_f32 ? prefix_run<64, float>(a, o, c.ldo, c.lse, st) : prefix_run<64, bf16>(a, o, c.ldo, c.lse, st);
+  return c.q_f32 ? GPT2_ERR_UNSUPPORTED_SHAPE : prefix_run<128, bf16>(a, o, c.ldo, c.lse, st);
+}
+
+int prefix_attention_f32(const float* q, const float* pk, const float* pv, int P, long pcap, const float* k,
+                         const float* v, const int32_t* len, int len_add, int max_len, int B, int H, int hd, float* o,
+                         cudaStream_t st) {
+  const dim3 grid(H, B);
+  const float scale = 1.f / sqrtf((float)hd);
+  if (hd == 64)
+    CUDA_TRY(launch_k(prefix_f32_kernel<64>, grid, 32, 0, st, q, pk, pv, P, pcap, k, v, len, len_add, max_len, H, scale,
+                      o));
+  else if (hd == 16)
+    CUDA_TRY(launch_k(prefix_f32_kernel<16>, grid, 32, 0, st, q, pk, pv, P, pcap, k, v, len, len_add, max_len, H, scale,
+                      o));
+  else
+    return GPT2_ERR_UNSUPPORTED_SHAPE;
+  LAUNCH_CHECK();
+  return GPT2_OK;
+}
+
+extern "C" {
+
+size_t gpt2_op_prefix_attention_scratch_bytes(int B, int Hq, int Hkv, int hd, int prefix_len, int max_len) {
+  return prefix_scratch_bytes(B, Hq, Hkv, hd, prefix_len, max_len);
+}
+
+int gpt2_op_prefix_attention_bf16(const uint16_t* q, int ldq, const uint16_t* pk, const uint16_t* pv, int prefix_len,
+                                  int prefix_cap, const uint16_t* k, const uint16_t* v, const int32_t* len, int max_len,
+                                  uint16_t* o, int ldo, float* lse, void* scratch, size_t scratch_bytes, int B, int Hq,
+                                  int Hkv, int hd, void* stream) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || prefix_len < 0 || prefix_cap < prefix_len || max_len < 0)
+    return GPT2_ERR_INVALID_ARG;
+  if (!q || !o || !scratch || (prefix_len && (!pk || !pv)) || (max_len && (!k || !v || !len)))
+    return GPT2_ERR_INVALID_ARG;
+  if (((uintptr_t)q | (uintptr_t)o | (uintptr_t)lse | (uintptr_t)len) & 3) return GPT2_ERR_INVALID_ARG;
+  if ((((uintptr_t)pk | (uintptr_t)pv) & 15 && prefix_len) || (((uintptr_t)k | (uintptr_t)v) & 15 && max_len))
+    return GPT2_ERR_INVALID_ARG;
+  if ((uintptr_t)scratch & 15) return GPT2_ERR_INVALID_ARG;
+  if (hd != 16 && hd != 64 && hd != 128) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  if (Hq % Hkv) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  if (ldq < (long)Hq * hd || ldo < (long)Hq * hd || ldq % 2 || ldo % 2) return GPT2_ERR_INVALID_ARG;
+  if (B == 0) return GPT2_OK;
+  PrefixAttn c = {};
+  c.q = q; c.ldq = ldq; c.pk = pk; c.pv = pv; c.P = prefix_len; c.pcap = prefix_cap;
+  c.k = k; c.v = v; c.len = len; c.max_len = max_len;
+  c.o = o; c.ldo = ldo; c.lse = lse; c.scratch = scratch; c.scratch_bytes = scratch_bytes;
+  c.B = B; c.Hq = Hq; c.Hkv = Hkv; c.hd = hd;
+  return prefix_attention(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

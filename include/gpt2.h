@@ -284,6 +284,89 @@ int gpt2_greedy_next(gpt2_ctx* ctx, const float* logits, int batch, int32_t* nex
                      void* stream);
 
 /* ------------------------------------------------------------------------
+ * What a served batch adds to the decode step: 4-bit weights, a prefix that
+ * all rows share, and rules on the logits ("Criei GPT-2 do zero com uma RTX
+ * 4090", section "Conversando de verdade com ele": every conversation starts
+ * with the same instructions and is continued one token at a time).
+ * ---------------------------------------------------------------------- */
+
+/* 4-bit weights of the model for decoding: the matrices of every layer (w_qkv,
+ * w_o, w_fc, w_mp) and wte as the LM head, each quantised as
+ * gpt2_op_q4_quantize does with groups of `group` (32, 64 or 128, dividing
+ * d_model) consecutive inputs.  Biases, LayerNorms and the embeddings stay as
+ * they are.  gpt2_q4_bytes: size of the buffer; 0 for an invalid
+ * configuration or group, and for mode 1 (the fp32 correctness mode has no
+ * 4-bit form). */
+size_t gpt2_q4_bytes(const gpt2_config* cfg, int group);
+
+/* Quantises the context's fp32 master weights into q4 (device, 256-byte
+ * aligned, q4_bytes >= gpt2_q4_bytes, else GPT2_ERR_WORKSPACE).  To be called
+ * again after the weights change. */
+int gpt2_q4_pack(gpt2_ctx* ctx, void* q4, size_t q4_bytes, int group, void* stream);
+
+/* Options of gpt2_decode_step_ex; a zeroed struct asks for nothing. */
+typedef struct {
+  const void* q4;         /* 4-bit weights (gpt2_q4_pack) in place of the shadow's, or NULL */
+  size_t q4_bytes;
+  int q4_group;
+  const void* prefix;     /* a cache of one sequence, sized for (1, prefix_cap), whose first prefix_len */
+  size_t prefix_bytes;    /*   positions precede every row's own, or NULL */
+  int prefix_cap;
+  int prefix_len;         /* 0 <= prefix_len <= prefix_cap, prefix_len + max_len <= n_ctx */
+  void* scratch;          /* device, 256-byte aligned, gpt2_decode_scratch_bytes; NULL without a prefix */
+  size_t scratch_bytes;
+} gpt2_decode_opts;
+
+/* Scratch of a step of `batch` rows with caches of max_len positions behind a
+ * prefix of prefix_len (0 without a prefix or for invalid sizes). */
+size_t gpt2_decode_scratch_bytes(const gpt2_config* cfg, int batch, int max_len, int prefix_len);
+
+/* gpt2_decode_step with options (NULL: exactly gpt2_decode_step).  With a
+ * prefix, row b's token sits at position prefix_len + pos[b] of its sequence
+ * and attends to the prefix and to the row's own positions 0..pos[b]; the
+ * prefix cache is only read, so several batches may share it, and a row's
+ * own cache holds nothing of it.  pos[b] still counts the row's own
+ * positions (0 <= pos[b] < max_len).  In modes 0 and 2 the queries and the
+ * attention's output are then rounded to bf16, as in the forward.  Steps in
+ * flight at the same time need scratch of their own, captured graphs among
+ * them. */
+int gpt2_decode_step_ex(gpt2_ctx* ctx, void* cache, size_t cache_bytes, int batch, int max_len,
+                        const int32_t* tokens, const int32_t* pos, const gpt2_decode_opts* opts, float* logits,
+                        void* stream);
+
+/* Rules on logits, one set per row; device arrays, any of them NULL where the
+ * rule is not asked for.  With c[v] the occurrences of id v at places gen_start[r]
+ * and above of the row's history, in this order, each step rounded to fp32:
+ *   z = v anywhere in the history ? (z > 0 ? z / repetition : z * repetition) : z
+ *   z = (z - frequency * c[v]) - (c[v] > 0 ? presence : 0)
+ *   z = z + bias of v            (of several entries of an id the last counts)
+ *   z = -inf unless v is allowed
+ * Ids outside the vocabulary (-1, say) in history or bias_ids are skipped. */
+typedef struct {
+  int32_t* history;          /* [rows, history_ld] ids; the first history_len[r] count */
+  int32_t* history_len;      /* [rows]; clamped to 0..history_ld */
+  const int32_t* gen_start;  /* [rows]: first place of the generated ids; NULL: 0 */
+  const float* repetition;   /* [rows]; NULL: 1 */
+  const float* presence;     /* [rows]; NULL: 0 */
+  const float* frequency;    /* [rows]; NULL: 0 */
+  const int32_t* bias_ids;   /* [rows, n_bias] */
+  const float* bias_values;  /* [rows, n_bias] */
+  const uint32_t* allowed;   /* [rows, allowed_ld] words: bit v % 32 of word v / 32 set where v is allowed */
+  int history_ld;
+  int n_bias;                /* at most 4096 */
+  int allowed_ld;            /* at least ceil(vocab / 32) */
+  int append;                /* 1: the chosen id is added to history where there is room (history_len + 1) */
+} gpt2_logit_rules;
+
+/* gpt2_greedy_next under rules: logits (device fp32 [batch, vocab_padded]) are
+ * rewritten in place over ids < vocab_real, next_tokens[b] is the greedy
+ * choice of what is left (id 0 where nothing is above -inf), pos as there.
+ * The state of the rules lives on the device, so a loop of steps can be
+ * captured in one CUDA graph. */
+int gpt2_rules_next(gpt2_ctx* ctx, float* logits, int batch, const gpt2_logit_rules* rules, int32_t* next_tokens,
+                    int32_t* pos, void* stream);
+
+/* ------------------------------------------------------------------------
  * Single-operation entry points used by the kernel unit tests.  They run the
  * same kernels the step runs, on caller buffers.
  * ---------------------------------------------------------------------- */
@@ -419,6 +502,67 @@ int gpt2_op_lm_head_ce_fwd_bf16(const uint16_t* x, const uint16_t* w, const int3
 int gpt2_op_lm_head_ce_bwd_bf16(const uint16_t* x, const uint16_t* w, int M, int V, int d, float grad_scale,
                                 uint16_t* dx, float* dw, int accumulate, void* scratch, size_t scratch_bytes,
                                 void* stream);
+
+/* ---- 4-bit weights with group scales --------------------------------------
+ * A linear layer's weight [N, K] as signed 4-bit numbers with one scale per
+ * group of `group` (32, 64 or 128; K a multiple of it) consecutive inputs:
+ *   s[n, j] = bf16(max over group j of |w[n, k]| / 7)
+ *   q[n, k] = clamp(rint(w[n, k] / s[n, j]), -7, 7), 0 where s is 0
+ * (fp32 arithmetic, ties to even).  packed: N rows of K / 2 bytes, byte i
+ * holding q + 8 of inputs 2i (low half) and 2i + 1.  scales: bf16 [K / group]
+ * rows of N rounded up to a multiple of 8 (the added columns are written 0).
+ * A group that holds an infinity or NaN gets such a scale.  Matrix buffers are
+ * 16-byte aligned. */
+size_t gpt2_op_q4_packed_bytes(int N, int K);             /* 0 for invalid sizes */
+size_t gpt2_op_q4_scale_count(int N, int K, int group);   /* elements; 0 for invalid sizes */
+
+/* w: bf16, or fp32 where w_fp32, [N, ldw]; ldw a multiple of 8.  Errors:
+ * INVALID_ARG for NULL or misaligned buffers, negative sizes or ldw < K;
+ * UNSUPPORTED_SHAPE for a group or multiples other than those above. */
+int gpt2_op_q4_quantize(const void* w, int w_fp32, int ldw, int N, int K, int group, uint8_t* packed,
+                        uint16_t* scales, void* stream);
+
+/* The values s q back, as bf16 (rounded once) or fp32, [N, ldo]; ldo a
+ * multiple of 8.  Nibble 0 (which the quantiser does not write) is -8. */
+int gpt2_op_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int N, int K, int group, void* out,
+                          int out_fp32, int ldo, void* stream);
+
+/* out[r, n] = sum_k s[n, k / group] q[n, k] x[r, k] (+ bias[n]) for 1 to 16
+ * rows, the linear layer of a decode step.  x bf16 [rows, ldx] (ldx a multiple
+ * of 8, 16-byte aligned), bias bf16 [N] or NULL, out bf16 or fp32 [rows, ldo],
+ * any N and ldo >= N.  Products are exact and summed in fp32, in an order that
+ * depends on the sizes only.  K at most 32768.  Errors as above; rows > 16 is
+ * INVALID_ARG. */
+int gpt2_op_gemv_q4(const uint16_t* x, int ldx, const uint8_t* packed, const uint16_t* scales, const uint16_t* bias,
+                    void* out, int out_fp32, int ldo, int rows, int N, int K, int group, void* stream);
+
+/* ---- attention over a shared prefix ----------------------------------------
+ * One new token per sequence: query head h of row b attends to the
+ * prefix_len keys of its key/value head h / (Hq / Hkv) in the prefix, which
+ * is the same for all rows and read once, and to the first len[b] keys of the
+ * row's own cache:
+ *   o[b, h] = softmax(q . k / sqrt(hd)) v,  lse[b, h] = log sum exp(q . k / sqrt(hd))
+ * q, o bf16 [B, Hq * hd] with row pitches ldq, ldo (even, 4-byte aligned);
+ * pk, pv bf16 [Hkv][prefix_cap][hd]; k, v bf16 [B][Hkv][max_len][hd] (16-byte
+ * aligned); len device int32 [B], clamped to 0..max_len; lse fp32 [B, Hq] or
+ * NULL.  hd 16, 64 or 128, Hq a multiple of Hkv.  prefix_len or max_len 0: that
+ * part's pointers may be NULL.  A row without any key gets o = 0, lse = -inf.
+ * Keys past prefix_len or len[b] are not read.  scratch: device, 16-byte
+ * aligned, at least the given bytes (0 for invalid sizes); calls in flight at
+ * the same time need scratch of their own.  Sums are in a fixed order. */
+size_t gpt2_op_prefix_attention_scratch_bytes(int B, int Hq, int Hkv, int hd, int prefix_len, int max_len);
+int gpt2_op_prefix_attention_bf16(const uint16_t* q, int ldq, const uint16_t* pk, const uint16_t* pv, int prefix_len,
+                                  int prefix_cap, const uint16_t* k, const uint16_t* v, const int32_t* len, int max_len,
+                                  uint16_t* o, int ldo, float* lse, void* scratch, size_t scratch_bytes, int B, int Hq,
+                                  int Hkv, int hd, void* stream);
+
+/* Rules on logits (see gpt2_logit_rules) for any number of rows: out[r, v] for
+ * v < vocab from logits[r, v] (fp32, row pitches ldo and ld; the same buffer
+ * and pitch for an update in place; columns past vocab are left as they were),
+ * next[r] (NULL: none) the greedy choice as gpt2_rules_next, pos[r] += 1 (NULL:
+ * none; only with next).  vocab at most 392960. */
+int gpt2_op_logit_rules(const float* logits, int ld, float* out, int ldo, int rows, int vocab,
+                        const gpt2_logit_rules* rules, int32_t* next, int32_t* pos, void* stream);
 
 /* ------------------------------------------------------------------------
  * The micro-step as a CUDA graph.  A step launches about 300 kernels; issued

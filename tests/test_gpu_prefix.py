@@ -1,0 +1,164 @@
+"""Attention over a shared prefix and each row's own positions against its
+definition in 64 bits.
+
+Tolerance of o: the probabilities are rounded to bf16 before the second
+product, half a step (2^-8 relative) each, so o is off by at most
+2^-8 sum p |v|; the fp32 sums and exponentials add less than 2^-14 of the same
+(2^-22 a step over the longest chain of steps here), a score off by s changes
+a probability by a share 2 s at most, and o itself is rounded once, 2^-8 |o|.
+lse: a score's hd products are exact, their sum off by 2^-23 of their
+magnitudes each time; the sum of the exponentials as above.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import decoder_only_transformer_step_b200 as gp
+
+pytestmark = pytest.mark.gpu
+
+
+def make(B, Hq, Hkv, hd, P, max_len, lens, seed, cap=None, ldq=None, ldo=None, q_std=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def rnd(*s):
+        return torch.empty(s, device="cuda").normal_(generator=g).bfloat16()
+    cap = cap or P
+    ldq, ldo = ldq or Hq * hd, ldo or Hq * hd
+    s = dict(B=B, Hq=Hq, Hkv=Hkv, hd=hd, P=P, cap=cap, max_len=max_len, ldq=ldq, ldo=ldo, lens=lens)
+    s["q"] = rnd(B, ldq) * q_std
+    s["pk"], s["pv"] = rnd(Hkv, cap, hd), rnd(Hkv, cap, hd)
+    s["k"], s["v"] = rnd(B, Hkv, max_len, hd), rnd(B, Hkv, max_len, hd)
+    s["len"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    s["o"] = torch.full((B, ldo), 55.0, dtype=torch.bfloat16, device="cuda")
+    s["lse"] = torch.full((B, Hq), 9.0, device="cuda")
+    n = gp.gpt2_op_prefix_attention_scratch_bytes(B, Hq, Hkv, hd, P, max_len)
+    s["scratch"] = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN where nothing is written
+    return s
+
+
+def call(s, stream=None):
+    gp.gpt2_op_prefix_attention_bf16(s["q"], s["ldq"], s["pk"], s["pv"], s["P"], s["cap"], s["k"], s["v"], s["len"],
+                                     s["max_len"], s["o"], s["ldo"], s["lse"], s["scratch"], s["B"], s["Hq"], s["Hkv"],
+                                     s["hd"], stream=stream)
+
+
+def check(s):
+    B, Hq, Hkv, hd, P = (s[k] for k in ("B", "Hq", "Hkv", "hd", "P"))
+    G = Hq // Hkv
+    q = s["q"][:, : Hq * hd].double().view(B, Hq, hd)
+    o = s["o"][:, : Hq * hd].double().view(B, Hq, hd)
+    for b in range(B):
+        n = max(0, min(s["max_len"], s["lens"][b]))
+        if P + n == 0:
+            assert bool((o[b] == 0).all()) and bool((s["lse"][b] == -math.inf).all())
+            continue
+        k = torch.cat((s["pk"][:, :P].double(), s["k"][b, :, :n].double()), 1).repeat_interleave(G, 0)
+        v = torch.cat((s["pv"][:, :P].double(), s["v"][b, :, :n].double()), 1).repeat_interleave(G, 0)
+        z = torch.einsum("hd,hjd->hj", q[b], k) / math.sqrt(hd)
+        mag = torch.einsum("hd,hjd->hj", q[b].abs(), k.abs()).amax(1) / math.sqrt(hd)
+        p = torch.softmax(z, 1)
+        want = torch.einsum("hj,hjd->hd", p, v)
+        sc = (hd + 4) * 2.0**-23 * mag  # how far a score may be off
+        tol = (2.0**-8 + 2.0**-14 + 4 * sc[:, None]) * torch.einsum("hj,hjd->hd", p, v.abs()) + 2.0**-8 * want.abs()
+        err = (o[b] - want).abs()
+        assert bool((err <= tol).all()), (b, float((err / tol).max()))
+        lse = torch.logsumexp(z, 1)
+        assert bool(((s["lse"][b].double() - lse).abs() <= 2 * sc + 2.0**-18 + 2.0**-22 * lse.abs()).all()), b
+    assert bool((s["o"][:, Hq * hd:] == 55).all())
+
+
+@pytest.mark.parametrize("hd", [16, 64, 128])
+@pytest.mark.parametrize("P", [0, 1, 31, 129, 700])
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 2, 2), (3, 4, 2), (5, 3, 1), (17, 8, 8), (9, 40, 2)])
+def test_prefix_attention_against_64_bits(hd, P, B, Hq, Hkv):
+    max_len = 70
+    lens = [(37 * b) % (max_len + 1) for b in range(B)]       # 0 and others
+    lens[-1] = max_len
+    s = make(B, Hq, Hkv, hd, P, max_len, lens, seed=P + B, cap=P + 3, ldq=Hq * hd + 6, ldo=Hq * hd + 2)
+    # what lies behind the keys that count is not read
+    s["pk"][:, P:] = float("nan")
+    s["pv"][:, P:] = float("inf")
+    for b, n in enumerate(lens):
+        s["k"][b, :, n:] = float("nan")
+        s["v"][b, :, n:] = float("-inf")
+    call(s)
+    check(s)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,hd,P,max_len", [(33, 32, 8, 128, 3000, 40), (64, 8, 1, 64, 2049, 9),
+                                                   (200, 4, 4, 64, 511, 33), (2, 64, 1, 128, 5000, 600),
+                                                   (16, 12, 12, 64, 3500, 596), (1, 1, 1, 64, 40000, 1)])
+def test_many_rows_and_long_prefixes(B, Hq, Hkv, hd, P, max_len):
+    s = make(B, Hq, Hkv, hd, P, max_len, [(b * 13) % (max_len + 1) for b in range(B)], seed=B)
+    call(s)
+    check(s)
+
+
+def test_sharp_scores_and_lengths_out_of_range():
+    # scores of +-60: one key takes nearly all weight; lengths below 0 and past max_len are clamped
+    s = make(4, 4, 4, 64, 257, 40, [-5, 0, 41, 1 << 30], seed=1, q_std=8.0)
+    call(s)
+    check(s)
+
+
+def test_no_keys_at_all_and_null_parts():
+    s = make(2, 4, 4, 64, 0, 0, [0, 0], seed=2)
+    s["pk"] = s["pv"] = s["k"] = s["v"] = s["len"] = None
+    call(s)
+    assert bool((s["o"] == 0).all()) and bool((s["lse"] == -math.inf).all())
+
+
+def test_without_own_positions_or_lse():
+    s = make(3, 4, 4, 64, 300, 0, [0, 0, 0], seed=3)
+    s["lse"] = None
+    call(s)
+    s["lse"] = torch.zeros(3, 4, device="cuda")
+    o = s["o"].clone()
+    call(s)
+    assert torch.equal(o, s["o"])
+    check(s)
+
+
+def test_it_repeats_bitwise_and_in_a_graph_whose_lengths_grow():
+    s = make(5, 12, 12, 64, 600, 300, [0, 7, 100, 299, 300], seed=4)
+    call(s)
+    o, lse = s["o"].clone(), s["lse"].clone()
+    s["scratch"].fill_(0xFF)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(s, stream=side)
+    side.synchronize()
+    assert torch.equal(o, s["o"]) and torch.equal(lse, s["lse"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(s)
+    s["lens"] = [1, 8, 101, 300, 300]
+    s["len"].copy_(torch.tensor(s["lens"], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    check(s)
+
+
+def test_a_cache_whose_offsets_pass_32_bits():
+    # 2^31 elements and more before the last head's keys and the last row's own
+    B, H, hd, cap = 1, 9, 128, 1 << 21
+    k = torch.zeros(H, cap, hd, dtype=torch.bfloat16, device="cuda")
+    s = make(B, H, H, hd, 200, 1, [0], seed=5)
+    k[:, :200] = s["pk"]
+    s["pk"] = s["pv"] = k
+    s["cap"] = cap
+    call(s)
+    check(s)
+    own = torch.zeros(9, 1, cap, hd, dtype=torch.bfloat16, device="cuda")
+    s = make(9, 1, 1, hd, 0, 4, [0, 1, 0, 2, 0, 3, 0, 0, 100], seed=6)
+    own[:, :, :100] = torch.randn(9, 1, 100, hd, device="cuda").bfloat16()
+    s["k"] = s["v"] = own
+    s["max_len"] = cap
+    s["scratch"] = torch.empty(gp.gpt2_op_prefix_attention_scratch_bytes(9, 1, 1, hd, 0, cap), dtype=torch.uint8,
+                               device="cuda")
+    call(s)
+    check(s)

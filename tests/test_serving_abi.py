@@ -1,0 +1,133 @@
+"""Refusals and sizes of the serving operators (4-bit weights, attention over a
+shared prefix, rules on logits), all decided on the host: no GPU needed."""
+import ctypes
+
+import pytest
+
+import decoder_only_transformer_step_b200 as gp
+from decoder_only_transformer_step_b200 import build_lib
+
+INVALID = gp.ERRORS_BY_NAME["GPT2_ERR_INVALID_ARG"]
+SHAPE = gp.ERRORS_BY_NAME["GPT2_ERR_UNSUPPORTED_SHAPE"]
+WORKSPACE = gp.ERRORS_BY_NAME["GPT2_ERR_WORKSPACE"]
+A = 1 << 20  # an aligned address that no call below gets to read
+
+
+@pytest.fixture(scope="module")
+def L():
+    build_lib.build()
+    return gp._lib()
+
+
+def test_q4_sizes(L):
+    assert gp.gpt2_op_q4_packed_bytes(5, 64) == 5 * 32
+    assert gp.gpt2_op_q4_scale_count(5, 64, 32) == 2 * 8
+    assert gp.gpt2_op_q4_scale_count(8, 128, 128) == 8
+    for n, k, g in [(0, 64, 32), (5, 0, 32), (5, 48, 32), (5, 96, 64), (5, 64, 16), (5, 64, 0), (-1, 64, 32)]:
+        assert gp.gpt2_op_q4_scale_count(n, k, g) == 0
+    assert gp.gpt2_op_q4_packed_bytes(70000, 65536) == 70000 * 32768  # past 32 bits
+
+
+def test_q4_model_bytes(L):
+    cfg = gp.GPT2_124M.c()
+    mats = [(3 * 768, 768), (768, 768), (4 * 768, 768), (768, 4 * 768)]
+    pad = lambda b: (b + 255) // 256 * 256  # noqa: E731
+    for g in (32, 64, 128):
+        one = lambda n, k: pad(n * k // 2) + pad(k // g * n * 2)  # noqa: E731
+        assert gp.gpt2_q4_bytes(cfg, g) == 12 * sum(one(*m) for m in mats) + one(50304, 768)
+    assert gp.gpt2_q4_bytes(cfg, 48) == 0
+    assert gp.gpt2_q4_bytes(gp.GPT2_1558M.c(), 128) == 0      # d 1600 is no multiple of 128
+    assert gp.gpt2_q4_bytes(gp.GPT2_1558M.c(), 64) > 0
+    assert gp.gpt2_q4_bytes(gp.GPT2_TINY.c(), 32) == 0        # fp32 mode
+
+
+def test_quantize_refusals(L):
+    def q(w=A, w32=1, ldw=64, N=4, K=64, g=32, p=A, s=A):
+        return L.gpt2_op_q4_quantize(w, w32, ldw, N, K, g, p, s, None)
+    assert q(w=None) == q(p=None) == q(s=None) == INVALID
+    assert q(w=A + 4) == q(p=A + 8) == q(s=A + 2) == INVALID
+    assert q(N=-1) == q(K=-64) == q(ldw=32) == INVALID
+    assert q(K=48) == q(g=48) == q(g=0) == q(ldw=68) == q(K=0) == SHAPE
+    assert q(N=0) == 0
+
+    def d(p=A, s=A, N=4, K=64, g=32, o=A, ldo=64):
+        return L.gpt2_op_q4_dequantize(p, s, N, K, g, o, 0, ldo, None)
+    assert d(p=None) == d(s=None) == d(o=None) == d(o=A + 4) == d(ldo=32) == d(N=-2) == INVALID
+    assert d(K=80, ldo=80) == d(ldo=65) == d(g=16) == SHAPE
+    assert d(N=0) == 0
+
+
+def test_gemv_refusals(L):
+    def f(x=A, ldx=64, p=A, s=A, b=None, o=A, o32=0, ldo=8, rows=1, N=8, K=64, g=32):
+        return L.gpt2_op_gemv_q4(x, ldx, p, s, b, o, o32, ldo, rows, N, K, g, None)
+    assert f(x=None) == f(p=None) == f(s=None) == f(o=None) == INVALID
+    assert f(rows=17) == f(rows=-1) == f(N=-1) == f(ldx=32) == f(ldo=7) == INVALID
+    assert f(x=A + 8) == f(p=A + 4) == f(s=A + 2) == f(b=A + 1) == f(o=A + 1) == f(o=A + 2, o32=1) == INVALID
+    assert f(K=48) == f(g=40) == f(ldx=68) == f(K=0) == SHAPE
+    assert f(K=32768 + 32, ldx=40000) == SHAPE
+    assert f(rows=0) == f(N=0) == 0
+
+
+def test_prefix_refusals_and_scratch(L):
+    size = gp.gpt2_op_prefix_attention_scratch_bytes
+    assert size(2, 4, 4, 64, 100, 10) > 0
+    for a in [(0, 4, 4, 64, 1, 1), (2, 4, 3, 64, 1, 1), (2, 4, 4, 32, 1, 1), (2, 4, 4, 64, -1, 1), (2, 4, 4, 64, 1, -1)]:
+        assert size(*a) == 0
+    assert size(1, 1, 1, 64, 0, 0) > 0
+
+    def f(q=A, ldq=256, pk=A, pv=A, P=8, cap=8, k=A, v=A, n=A, m=4, o=A, ldo=256, lse=None, s=A, sb=1 << 40, B=2, Hq=4,
+          Hkv=4, hd=64):
+        return L.gpt2_op_prefix_attention_bf16(q, ldq, pk, pv, P, cap, k, v, n, m, o, ldo, lse, s, sb, B, Hq, Hkv, hd,
+                                               None)
+    assert f(q=None) == f(pk=None) == f(pv=None) == f(k=None) == f(v=None) == f(n=None) == f(o=None) == f(s=None) == INVALID
+    assert f(cap=7) == f(P=-1) == f(m=-1) == f(B=-1) == f(Hkv=0) == f(Hq=0) == INVALID
+    assert f(ldq=255) == f(ldo=128) == f(ldq=257) == f(ldo=257) == INVALID
+    assert f(q=A + 2) == f(o=A + 2) == f(pk=A + 8) == f(v=A + 8) == f(lse=A + 2) == f(s=A + 8) == INVALID
+    assert f(hd=32) == f(Hq=6, Hkv=4) == SHAPE
+    assert f(sb=size(2, 4, 4, 64, 8, 4) - 1) == WORKSPACE
+    assert f(B=0) == 0
+
+
+def test_logit_rules_refusals(L):
+    def f(z=A, ld=100, o=A, ldo=100, rows=2, V=100, nxt=A, pos=None, null=False, **r):
+        c = gp.gpt2_logit_rules(**r)
+        return L.gpt2_op_logit_rules(z, ld, o, ldo, rows, V, None if null else ctypes.byref(c), nxt, pos, None)
+    assert f(z=None) == f(o=None) == f(null=True) == f(ld=99) == f(ldo=99) == f(rows=-1) == f(V=-1) == INVALID
+    assert f(ldo=101) == INVALID                                   # in place with another pitch
+    assert f(nxt=None, pos=A) == INVALID
+    assert f(history=A) == f(history=A, history_len=A) == INVALID  # no lengths, no pitch
+    assert f(append=1) == f(nxt=None, history=A, history_len=A, history_ld=4, append=1) == INVALID
+    assert f(n_bias=3) == f(n_bias=-1) == f(n_bias=2, bias_ids=A) == INVALID
+    assert f(allowed=A, allowed_ld=3) == f(presence=A + 2) == f(z=A + 1) == INVALID
+    assert f(n_bias=4097, bias_ids=A, bias_values=A) == SHAPE
+    assert f(V=392961, ld=400000, ldo=400000) == SHAPE
+    assert f(rows=0) == f(V=0) == 0
+
+
+def test_model_calls_refuse_a_null_context(L):
+    assert L.gpt2_q4_pack(None, A, 1 << 30, 64, None) == INVALID
+    assert L.gpt2_decode_step_ex(None, A, 1 << 30, 1, 1, A, A, None, A, None) == INVALID
+    assert L.gpt2_rules_next(None, A, 1, ctypes.byref(gp.gpt2_logit_rules()), A, None, None) == INVALID
+    cfg = gp.GPT2_124M.c()
+    assert gp.gpt2_decode_scratch_bytes(cfg, 16, 100, 500) == gp.gpt2_op_prefix_attention_scratch_bytes(16, 12, 12, 64, 500, 100)
+    for a in [(17, 100, 500), (16, 100, 925), (16, 0, 500), (16, 100, 0)]:
+        assert gp.gpt2_decode_scratch_bytes(cfg, *a) == 0
+
+
+def test_binding_refuses_host_short_and_mistyped_buffers(L):
+    import torch
+    x = torch.zeros(64, dtype=torch.bfloat16)
+    p, s = torch.zeros(8 * 32, dtype=torch.uint8), torch.zeros(16, dtype=torch.bfloat16)
+    o = torch.zeros(8, dtype=torch.bfloat16)
+    with pytest.raises(gp.Gpt2Error, match="not on the current CUDA device"):
+        gp.gpt2_op_gemv_q4(x, 64, p, s, None, o, 0, 8, 1, 8, 64, 32)
+    with pytest.raises(gp.Gpt2Error, match="x is torch.float32"):
+        gp.gpt2_op_gemv_q4(x.float(), 64, p, s, None, o, 0, 8, 1, 8, 64, 32)
+    with pytest.raises(gp.Gpt2Error, match="is missing"):
+        gp.gpt2_op_gemv_q4(None, 64, p, s, None, o, 0, 8, 1, 8, 64, 32)
+    with pytest.raises(gp.Gpt2Error, match="belong together"):
+        gp.LogitRules(bias_ids=torch.zeros(1, 2, dtype=torch.int32))
+    with pytest.raises(gp.Gpt2Error, match="needs history_len"):
+        gp.LogitRules(history=torch.zeros(1, 2, dtype=torch.int32))
+    with pytest.raises(gp.Gpt2Error, match="rules are for"):
+        gp.LogitRules(presence=torch.zeros(2), frequency=torch.zeros(3))
