@@ -9,6 +9,8 @@
 // Storage: nibbles q + 8, byte j of a row holding k = 2j (low half) and
 // 2j + 1; scales group-major [K / group][pitch], pitch = N rounded up to 8, so
 // that the scales of a tile of output columns are consecutive.
+#include <stdlib.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -22,14 +24,35 @@ namespace {
 // half a byte out.
 constexpr int QZ_ROWS = 32, QZ_K = 256;
 
-// rint(w / s), the division as IEEE rounds it: the product with the reciprocal
-// r = 1 / s is within 7 * 2^-22 < 1e-5 of the quotient, so that the integers
-// can differ only within that of a half; only there is the division made.
-DEVI int q4_round(float w, float s, float r) {
-  const float t = w * r;
-  float q = rintf(t);
-  if (!(fabsf(t - q) < 0.49999f)) q = rintf(w / s);
-  return __float2int_rn(fminf(fmaxf(q, -7.f), 7.f));
+// q + 8 of eight weights as nibbles, q = clamp(rint(w / s), -7, 7) with the
+// division as IEEE rounds it, r an approximate reciprocal of s (2 units in the
+// last place).  w r is within 7 * 2^-21 < 1e-5 of the quotient, so its nearest
+// integer can be another one only within that of a half: where the distance
+// from the integer is above 0.49999 (or a NaN) the division is made.  The
+// integers come out of the low bits of w r + 1.5 * 2^23.
+DEVI uint32_t q4_word(const float (&w)[8], float s, float r) {
+  constexpr float MAGIC = 12582912.f + 8.f;  // bits 0x4b400008
+  float far = 0.f, d[8];
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 7; e >= 0; --e) {
+    const float t = __fmaf_rn(w[e], r, MAGIC);
+    d[e] = fabsf(__fmaf_rn(w[e], r, -__fsub_rn(t, MAGIC)));
+    far = d[e] < 0.49999f ? far : 1.f;
+    word = word * 16u + __float_as_uint(t);
+  }
+  word -= 0x4b400000u * 0x11111111u;
+  // (a subnormal s can be so coarse that a quotient passes 7: with the others)
+  if (far == 0.f && s >= 0x1p-100f) return word;
+  const bool all = !(s >= 0x1p-100f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (all || !(d[e] < 0.49999f)) {
+      const int q = s == 0.f ? 0 : __float2int_rn(fminf(fmaxf(rintf(w[e] / s), -7.f), 7.f));
+      word = (word & ~(15u << (4 * e))) | ((uint32_t)(q + 8) << (4 * e));
+    }
+  }
+  return word;
 }
 
 template <typename T, int G>
@@ -41,41 +64,45 @@ __global__ void __launch_bounds__(256)
   pdl_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = blockIdx.x * QZ_ROWS, k0 = blockIdx.y * QZ_K, k = k0 + lane * 8;
-  float v[4][8];
+  constexpr int W4 = sizeof(T) / 2;  // 16-byte words of eight weights
+  uint4 raw[4][W4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = n0 + warp * 4 + i;
-    if (n < N && k < K) {
-      const T* p = w + (size_t)n * ldw + k;
-      if constexpr (sizeof(T) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        v[i][0] = bf16lo(u.x); v[i][1] = bf16hi(u.x); v[i][2] = bf16lo(u.y); v[i][3] = bf16hi(u.y);
-        v[i][4] = bf16lo(u.z); v[i][5] = bf16hi(u.z); v[i][6] = bf16lo(u.w); v[i][7] = bf16hi(u.w);
-      } else {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
-        v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
-      }
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    }
+    for (int h = 0; h < W4; ++h)
+      raw[i][h] = n < N && k < K ? reinterpret_cast<const uint4*>(w + (size_t)n * ldw + k)[h] : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // the largest magnitude as an unsigned integer: NaN above infinity above
     // every finite value, so that a group holding either gets such a scale
-    uint32_t top = 0;
+    uint32_t top;
+    float v[8];
+    if constexpr (sizeof(T) == 2) {
+      const uint4 u = raw[i][0];
+      top = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+      top = max(top & 0xffff0000u, top << 16);
+      v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
+      v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
+    } else {
+      const uint32_t x[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                             raw[i][W4 - 1].x, raw[i][W4 - 1].y, raw[i][W4 - 1].z, raw[i][W4 - 1].w};
+      top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
+      for (int e = 0; e < 8; ++e) {
+        top = max(top, x[e] & 0x7fffffffu);
+        v[e] = __uint_as_float(x[e]);
+      }
+    }
 #pragma unroll
     for (int o = LG / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const bf16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.f);
-    const float s = __bfloat162float(sb), r = 1.f / s;
+    const float s = __bfloat162float(sb);
     const int n = n0 + warp * 4 + i;
-    uint32_t word = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) word |= (uint32_t)((s == 0.f ? 0 : q4_round(v[i][e], s, r)) + 8) << (4 * e);
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const uint32_t word = q4_word(v, s, r);
     if (n < N && k < K) *reinterpret_cast<uint32_t*>(packed + ((size_t)n * K + k) / 2) = word;
     if (lane % LG == 0) sm[lane / LG][warp * 4 + i] = sb;
   }
@@ -88,8 +115,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // The values the nibbles stand for, s q (exact in fp32, rounded once to bf16
-// where T is bf16); one thread per 8 of them, 16 rows of a block sharing the
+// where T is bf16).  A warp takes 256 inputs of 8 rows, a lane 8 inputs of
+// each with all loads in flight together; the 64 rows of a block share the
 // sectors of the scales.
+constexpr int DQ_ROWS = 8;
 template <typename T>
 __global__ void __launch_bounds__(256)
     q4_dequantize_kernel(const uint8_t* packed, const bf16* scales, long pitch, int group_shift, int N, int K,
@@ -97,16 +126,22 @@ __global__ void __launch_bounds__(256)
   pdl_start();
   const int k = (blockIdx.y * 32 + (threadIdx.x & 31)) * 8;
   if (k >= K) return;
+  const int n0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * DQ_ROWS;
+  uint32_t w[DQ_ROWS];
+  float s[DQ_ROWS];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = blockIdx.x * 16 + (threadIdx.x >> 5) + 8 * i;
-    if (n >= N) continue;
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(packed + ((size_t)n * K + k) / 2);
-    const float s = to_f(scales[(size_t)(k >> group_shift) * pitch + n]);
+  for (int i = 0; i < DQ_ROWS; ++i) {
+    const int n = min(n0 + i, N - 1);
+    w[i] = *reinterpret_cast<const uint32_t*>(packed + ((size_t)n * K + k) / 2);
+    s[i] = to_f(scales[(size_t)(k >> group_shift) * pitch + n]);
+  }
+#pragma unroll
+  for (int i = 0; i < DQ_ROWS; ++i) {
+    if (n0 + i >= N) break;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = s * (float)((int)((u >> (4 * e)) & 15u) - 8);
-    T* p = out + (size_t)n * ldo + k;
+    for (int e = 0; e < 8; ++e) v[e] = s[i] * (float)((int)((w[i] >> (4 * e)) & 15u) - 8);
+    T* p = out + (size_t)(n0 + i) * ldo + k;
     if constexpr (sizeof(T) == 2) {
       *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -118,33 +153,41 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------- matrix-vector products --
-// Bound by HBM reads of the nibbles.  The products run on mma.sync m16n8k16
-// with the weights as A (16 output columns a warp tile) and the rows of x as
-// B: at 13e12 weights/s (the copy bandwidth) CUDA-core multiply-adds of even
-// one row would take more issue slots than there are, while a nibble reaches
-// the tensor core in 1.4 instructions: bf16 bits 0x4300 | nibble are
-// 128 + nibble, and one packed subtraction of 136 leaves q exactly.  The
-// products of a group are summed in fp32 by the tensor core, with exact
-// operands, and the group's sum is multiplied by its scale in fp32, so that
-// no weight is rounded again.
+// Bound by HBM reads of the nibbles, and next to that by the instructions that
+// bring them to the products: at the copy bandwidth 13e12 weights/s leave an
+// SM's four schedulers about three instructions for 32 weights.  So the
+// products run on mma.sync m16n8k16 with the weights as A (16 output columns
+// a warp tile) and the rows of x as B, and a nibble is not converted at all: a
+// bf16 whose upper byte is zero is its lower byte times 2^-133 (subnormal
+// numbers and the lowest normal ones lie on one line), which mma takes
+// exactly, so that one AND leaves two operands (a nibble in the upper half of
+// a byte counts 16-fold).  To match, each row of x is staged times the power
+// of two that brings its largest magnitude to 2^110, a sixteenth of that at
+// odd k: exact in bf16, but for numbers below 2^-230 of the row's largest.
+// The nibbles are q + 8, so a group's sum starts at -8 sum x instead of 0 (the
+// group sums of x are formed once, when x is staged).  A group's products are
+// summed in fp32 by the tensor core and multiplied by the group's scale in
+// fp32: no weight is rounded again.
+//
+// A lane's share of a stage's row is what its quad's mma need of one group at a
+// time: 16, 8 or 4 bytes for groups of 128, 64 or 32, so that a product never
+// crosses a group; the order of the inputs inside a group is the lanes' own,
+// and x is staged in it.
 //
 // A block is 16 warps.  KS of them share a tile of 16 columns, each taking
-// every KS-th stage of 128 inputs of the tile; their sums meet in shared memory in a
-// fixed order.  Each warp copies its own stages (16 rows x 64 bytes and their
+// every KS-th stage of 128 inputs; their sums meet in shared memory in a fixed
+// order.  Each warp copies its own stages (16 rows x 64 bytes and their
 // scales) into a ring of its own with cp.async, several ahead, across tile
-// borders: no block-wide wait stands in the stream.  The rows of x lie in
-// shared memory as bf16 in the order in which the nibbles of a word unpack
-// (0 4 1 5 2 6 3 7), so that a fragment is one 16-byte load.  Inputs too long
-// for shared memory are split over the blocks of a cluster (up to 8), whose
-// sums meet through distributed shared memory, again in a fixed order.
+// borders: no block-wide wait stands in the stream.  Inputs too long for
+// shared memory are split over the blocks of a cluster (up to 8), whose sums
+// meet through distributed shared memory, again in a fixed order.
 constexpr int Q4_WARPS = 16;
 constexpr int Q4_COLS = 16;                    // output columns of a tile (the mma M)
 constexpr int Q4_STAGE = 128;                  // inputs of a stage
-constexpr int Q4_ROWPITCH = Q4_STAGE / 2 + 16; // bytes of a staged row: 8 rows' words then lie in 32 banks
-constexpr int Q4_MAX_RING = 6;
 constexpr int Q4_MAX_SPLIT = 8;
-constexpr int Q4_PART_TILES = 16;              // tiles whose sums a cluster exchanges at once
+constexpr int Q4_PART_TILES = 8;               // tiles whose sums a cluster exchanges at once
 constexpr int Q4_MAX_K = 32768;                // widest input
+constexpr int Q4_UNITS = 16;                   // 8-input units of x a lane holds while staging
 constexpr int Q4_SMEM = 227 * 1024;
 
 struct Q4Args {
@@ -169,26 +212,50 @@ struct Q4Args {
 };
 enum Q4Epi : int { Q4_BF16 = 0, Q4_F32, Q4_QKV, Q4_RESID, Q4_GELU };
 
-template <int G> constexpr int q4_slot() { return Q4_COLS * Q4_ROWPITCH + Q4_STAGE / G * Q4_COLS * 2; }
-// elements of a staged row of x: an odd multiple of 64 bytes
-inline int q4_xpitch(int kr) { return kr % 64 ? kr : kr + 32; }
+// Shared memory of a block, in bytes: the rows of x, the group sums, the row
+// factors, the warps' sums (two buffers), the cluster's, the rings.
+__host__ __device__ inline int q4_xpitch(int kr) { return kr % 64 ? kr : kr + 32; }  // an odd multiple of 64 bytes
+// bytes of a staged row of nibbles: the pitch that spreads the lanes' 16-, 8- or 4-byte reads over all banks
+__host__ __device__ constexpr int q4_rowpitch(int group) { return group == 128 ? 64 : (group == 64 ? 96 : 80); }
+__host__ __device__ constexpr int q4_slot(int group) {
+  return Q4_COLS * q4_rowpitch(group) + Q4_STAGE / group * Q4_COLS * 2;
+}
+struct Q4Smem {
+  int xg, fac, red, part, ring;
+};
+__host__ __device__ inline Q4Smem q4_smem(int nr, int kr, int group, int split) {
+  Q4Smem m;
+  m.xg = nr * q4_xpitch(kr) * 2;
+  m.fac = m.xg + ((kr / group * nr * 4 + 15) & ~15);
+  m.red = m.fac + 16 * 16;
+  m.part = m.red + 2 * Q4_WARPS * (nr / 8) * 512;
+  m.ring = m.part + (split > 1 ? Q4_PART_TILES * (nr / 8) * 512 : 0);
+  return m;
+}
 
 DEVI void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 DEVI void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-DEVI void cp_wait(int pending) {  // at most `pending` of the newest groups still in flight
-  switch (pending) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-  }
+// All but the newest ring - 2 groups have landed (rings of 2, 4 and 6 slots).
+DEVI void cp_wait_ring(int ring) {
+  if (ring == 6) asm volatile("cp.async.wait_group 4;" ::: "memory");
+  else if (ring == 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-DEVI uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+// a lane's W words of a group (W 4, 2 or 1)
+template <int W> DEVI void lds_words(uint32_t a, uint32_t (&v)[W]) {
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
+  else if constexpr (W == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a) : "memory");
+}
+DEVI float2 lds64f(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
   return v;
 }
 DEVI float lds_bf16(uint32_t a) {
@@ -213,14 +280,6 @@ DEVI float4 ld_dsmem4(uint32_t addr, int rank) {
                : "memory");
   return v;
 }
-
-// nibbles i and i + 4 of w as bf16 q
-DEVI uint32_t q4_pair(uint32_t w, int i) {
-  const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-  const uint32_t c = 0x43084308u;
-  __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&c));
-  return *reinterpret_cast<uint32_t*>(&r);
-}
 DEVI void q4_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -228,57 +287,55 @@ DEVI void q4_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// eight fp32 / bf16 inputs, rounded to bf16, in the nibbles' order
-DEVI uint4 q4_order(const float4& a, const float4& b) {
-  return make_uint4(pack_bf16x2(a.x, b.x), pack_bf16x2(a.y, b.y), pack_bf16x2(a.z, b.z), pack_bf16x2(a.w, b.w));
-}
-DEVI uint4 q4_order(const uint4& u) {
-  return make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
-                    __byte_perm(u.y, u.w, 0x7632));
-}
 DEVI float4 q4_ld4(const bf16* p) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
   return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
 }
+DEVI uint4 q4_pack8(const float4& a, const float4& b) {
+  return make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+}
 
-// Inputs [k0, k0 + kn) of the rows -> xs [NR][xp] (rows past a.rows zero).
-template <int NR>
-DEVI void q4_stage_x(const Q4Args& a, bf16* xs, int xp, int k0, int kn, int warp, int lane) {
-  if (a.ln) {
-    // one warp a row, the row held in registers for its two statistics
-    // (K <= 2048; the LayerNorm'd inputs are never split: k0 = 0, kn = K)
-    constexpr int U = 8;
-    const int K8 = a.K / 8;
-    for (int r = warp; r < NR; r += Q4_WARPS) {
-      bf16* dst = xs + (size_t)r * xp;
-      if (r >= a.rows) {
-        for (int i = lane; i < K8; i += 32) *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
-        continue;
-      }
+// Inputs [k0, k0 + kn) of the rows -> xs [NR][xp], their group sums xg
+// [group][NR] and the rows' factors (both 16-byte slots of fac hold two
+// powers of two whose product undoes the row's scaling and the 2^-133).  One
+// or two warps a row; a lane holds its units (8 inputs, as bf16) in registers
+// from the load to the scaled store.
+template <int NR, int G>
+DEVI void q4_stage_x(const Q4Args& a, bf16* xs, int xp, float* xg, float* fac, uint32_t* wmax, int k0, int kn, int warp,
+                     int lane) {
+  constexpr int WPR = Q4_WARPS / NR;  // warps of a row
+  const int r = warp / WPR, part = warp % WPR, n8 = kn / 8;
+  uint4 v[Q4_UNITS];
+#pragma unroll
+  for (int u = 0; u < Q4_UNITS; ++u) v[u] = make_uint4(0u, 0u, 0u, 0u);
+  if (r < a.rows) {
+    if (a.ln) {
+      // (K <= 2048, never split: k0 = 0, kn = K.)  Every warp of the row
+      // holds all of it for the two statistics, and keeps its own part.
+      constexpr int U = 8;
       const float* src = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi;
-      float4 v[U][2];
+      float4 f[U][2];
       float s = 0.f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = lane + 32 * u;
-        v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < K8) {
-          v[u][0] = *reinterpret_cast<const float4*>(src + 8 * i);
-          v[u][1] = *reinterpret_cast<const float4*>(src + 8 * i + 4);
+        f[u][0] = f[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n8) {
+          f[u][0] = *reinterpret_cast<const float4*>(src + 8 * i);
+          f[u][1] = *reinterpret_cast<const float4*>(src + 8 * i + 4);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        s += ((v[u][0].x + v[u][0].y) + (v[u][0].z + v[u][0].w)) + ((v[u][1].x + v[u][1].y) + (v[u][1].z + v[u][1].w));
+        s += ((f[u][0].x + f[u][0].y) + (f[u][0].z + f[u][0].w)) + ((f[u][1].x + f[u][1].y) + (f[u][1].z + f[u][1].w));
       const float mu = warp_sum(s) / a.K;
       float q = 0.f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (lane + 32 * u < K8) {
+        if (lane + 32 * u < n8) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float t0 = v[u][h].x - mu, t1 = v[u][h].y - mu, t2 = v[u][h].z - mu, t3 = v[u][h].w - mu;
+            const float t0 = f[u][h].x - mu, t1 = f[u][h].y - mu, t2 = f[u][h].z - mu, t3 = f[u][h].w - mu;
             q += (t0 * t0 + t1 * t1) + (t2 * t2 + t3 * t3);
           }
         }
@@ -287,71 +344,127 @@ DEVI void q4_stage_x(const Q4Args& a, bf16* xs, int xp, int k0, int kn, int warp
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = lane + 32 * u;
-        if (i < K8) {
+        if (i < n8 && u % WPR == part) {
           float4 o[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float4 gg = q4_ld4(a.ln_g + 8 * i + 4 * h), bb = q4_ld4(a.ln_b + 8 * i + 4 * h);
-            o[h] = make_float4((v[u][h].x - mu) * rs * gg.x + bb.x, (v[u][h].y - mu) * rs * gg.y + bb.y,
-                               (v[u][h].z - mu) * rs * gg.z + bb.z, (v[u][h].w - mu) * rs * gg.w + bb.w);
+            o[h] = make_float4((f[u][h].x - mu) * rs * gg.x + bb.x, (f[u][h].y - mu) * rs * gg.y + bb.y,
+                               (f[u][h].z - mu) * rs * gg.z + bb.z, (f[u][h].w - mu) * rs * gg.w + bb.w);
           }
-          *reinterpret_cast<uint4*>(dst + 8 * i) = q4_order(o[0], o[1]);
+          v[u / WPR] = q4_pack8(o[0], o[1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < Q4_UNITS; ++u) {
+        const int i = lane + 32 * (u * WPR + part);
+        if (i < n8) {
+          if (a.in_f32) {
+            const float* p = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi + k0 + 8 * i;
+            v[u] = q4_pack8(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4));
+          } else {
+            v[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.in) + (size_t)r * a.ldi + k0 + 8 * i);
+          }
         }
       }
     }
-    return;
   }
-  constexpr int U = 8;  // loads in flight per thread
-  const int n8 = kn / 8, total = NR * n8, nthr = Q4_WARPS * 32;
-  for (int i0 = threadIdx.x; i0 < total; i0 += U * nthr) {
-    uint4 v[U];
+  // the row's largest magnitude, as the bits of a bf16
+  uint32_t m2 = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * nthr, r = i / n8, c = i - r * n8;
-      v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < total && r < a.rows) {
-        if (a.in_f32) {
-          const float* p = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi + k0 + 8 * c;
-          v[u] = q4_order(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4));
-        } else {
-          v[u] = q4_order(*reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.in) + (size_t)r * a.ldi + k0 +
-                                                          8 * c));
-        }
+  for (int u = 0; u < Q4_UNITS; ++u)
+    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu),
+                               __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu)));
+  uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+  if constexpr (WPR > 1) {
+    if (lane == 0) wmax[warp] = m;
+    __syncthreads();
+    m = max(wmax[r * WPR], wmax[r * WPR + 1]);
+  }
+  // 2^110 over the power of two at or below it (1 for a row of zeros, and for
+  // one that holds an infinity or NaN: its sums are not finite anyway)
+  const int ex = (int)(m >> 7), sh = m == 0 || ex == 255 ? 0 : 237 - ex;
+  const float f1 = __int_as_float((127 + sh / 2) << 23), f2 = __int_as_float((127 + (sh - sh / 2)) << 23);
+  if (lane == 0 && part == 0) {
+    const int un = 133 - sh;
+    fac[4 * r] = __int_as_float((127 + un / 2) << 23);
+    fac[4 * r + 1] = __int_as_float((127 + (un - un / 2)) << 23);
+  }
+#pragma unroll
+  for (int u = 0; u < Q4_UNITS; ++u) {
+    const int i0 = 32 * (u * WPR + part), i = i0 + lane;
+    if (i0 < n8) {  // (the same for the whole warp)
+      const float x[8] = {bf16lo(v[u].x), bf16hi(v[u].x), bf16lo(v[u].y), bf16hi(v[u].y),
+                          bf16lo(v[u].z), bf16hi(v[u].z), bf16lo(v[u].w), bf16hi(v[u].w)};
+      float y[8], s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = x[e] * f1 * f2;
+        s += y[e];
+        if (e & 1) y[e] *= 0.0625f;
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * nthr, r = i / n8, c = i - r * n8;
-      if (i < total) *reinterpret_cast<uint4*>(xs + (size_t)r * xp + 8 * c) = v[u];
+      for (int o = 1; o < G / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (i < n8) {
+        // in the order in which the nibbles of a word unpack
+        // (unit c of lane t in its group goes to place 4 c + t: a quad's reads are consecutive)
+        constexpr int W = G / 32;
+        const int in_g = i % (4 * W), at = i - in_g + 4 * (in_g % W) + in_g / W;
+        *reinterpret_cast<uint4*>(xs + (size_t)r * xp + 8 * at) =
+            make_uint4(pack_bf16x2(y[0], y[4]), pack_bf16x2(y[1], y[5]), pack_bf16x2(y[2], y[6]), pack_bf16x2(y[3], y[7]));
+        if (i % (G / 8) == 0) xg[i / (G / 8) * NR + r] = s * -0x1p-130f;
+      }
     }
   }
 }
 
-// The epilogue of one lane's four sums of an n-tile: columns n0 + g,
-// n0 + g + 8 (values 0 1, 2 3), rows r0 and r0 + 1 (values 0 2, 1 3).
-DEVI void q4_epilogue(const Q4Args& a, const float4& s, int n0, int g, int r0) {
+// The epilogue's operands of one lane, loaded ahead of the products: the
+// biases of columns n0 + g and n0 + g + 8, the old residuals.
+template <int NT> struct Q4Pre {
+  float b[2], x[NT][4];
+};
+template <int NT> DEVI void q4_preload(const Q4Args& a, Q4Pre<NT>& p, int n0, int g, int t) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + g + 8 * h;
+    p.b[h] = a.bias && n < a.N ? to_f(a.bias[n]) : 0.f;
+  }
+  if (a.epi == Q4_RESID) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + g + 8 * (i >> 1), r = 8 * m + 2 * t + (i & 1);
+        p.x[m][i] = n < a.N && r < a.rows ? reinterpret_cast<const float*>(a.out)[(size_t)r * a.ldo + n] : 0.f;
+      }
+  }
+}
+// One lane's four sums of n-tile m: columns n0 + g, n0 + g + 8 (values 0 1,
+// 2 3), rows 8 m + 2 t and the next (values 0 2, 1 3).
+template <int NT> DEVI void q4_epilogue(const Q4Args& a, const float4& s, const Q4Pre<NT>& p, int m, int n0, int g, int t) {
   const float v4[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int n = n0 + g + 8 * (i >> 1), r = r0 + (i & 1);
+    const int n = n0 + g + 8 * (i >> 1), r = 8 * m + 2 * t + (i & 1);
     if (n >= a.N || r >= a.rows) continue;
-    const float v = v4[i] + (a.bias ? to_f(a.bias[n]) : 0.f);
+    const float v = v4[i] + p.b[i >> 1];
     const size_t at = (size_t)r * a.ldo + n;
     float* of = reinterpret_cast<float*>(a.out);
     bf16* ob = reinterpret_cast<bf16*>(a.out);
     switch (a.epi) {
       case Q4_BF16: ob[at] = from_f<bf16>(v); break;
       case Q4_F32: of[at] = v; break;
-      case Q4_RESID: of[at] += v; break;
+      case Q4_RESID: of[at] = p.x[m][i] + v; break;
       case Q4_GELU: ob[at] = from_f<bf16>(gelu_f<false>(v)); break;
       default: {  // Q4_QKV: q to out, k and v into the cache at pos[r]
         if (n < a.d) {
           of[at] = v;
         } else {
-          const int kind = n >= 2 * a.d, nn = n - a.d - kind * a.d, p = a.pos[r];
-          if (p >= 0 && p < a.max_len) {
+          const int kind = n >= 2 * a.d, nn = n - a.d - kind * a.d, ps = a.pos[r];
+          if (ps >= 0 && ps < a.max_len) {
             bf16* plane = reinterpret_cast<bf16*>(kind ? a.vc : a.kc);
-            plane[(((size_t)r * a.H + nn / a.hd) * a.max_len + p) * a.hd + nn % a.hd] = from_f<bf16>(v);
+            plane[(((size_t)r * a.H + nn / a.hd) * a.max_len + ps) * a.hd + nn % a.hd] = from_f<bf16>(v);
           }
         }
       }
@@ -361,52 +474,79 @@ DEVI void q4_epilogue(const Q4Args& a, const float4& s, int n0, int g, int r0) {
 
 template <int NT, int G>
 __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_constant__ Q4Args a) {
-  extern __shared__ __align__(128) uint8_t q4_smem[];
+  extern __shared__ __align__(128) uint8_t q4_smem_buf[];
+  __shared__ uint32_t wmax[Q4_WARPS];
   constexpr int NR = 8 * NT;            // rows of x held
-  constexpr int SLOT = q4_slot<G>();
+  constexpr int SLOT = q4_slot(G), RP = q4_rowpitch(G);
   constexpr int GS = Q4_STAGE / G;      // groups of a stage
-  constexpr int CG = G / 32;            // 32-input chunks of a group
+  constexpr int W = G / 32;             // words a lane has of a group
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = a.split > 1 ? (int)cluster_ctarank() : 0;
   const int bx = blockIdx.x / a.split, gx = gridDim.x / a.split;
   const int k0 = rank * a.kr, kn = max(0, min(a.kr, a.K - k0));
-  const int xp = a.kr % 64 ? a.kr : a.kr + 32;
-  bf16* xs = reinterpret_cast<bf16*>(q4_smem);
-  float4* red = reinterpret_cast<float4*>(q4_smem + (size_t)NR * xp * 2);       // [2][warps][NT][32]
-  float4* part = red + 2 * Q4_WARPS * NT * 32;                                  // (split) [tiles][NT][32]
-  uint8_t* ring0 = reinterpret_cast<uint8_t*>(part + (a.split > 1 ? Q4_PART_TILES * NT * 32 : 0));
-  const uint32_t ring = smem_u32(ring0) + warp * a.ring * SLOT;
+  const int xp = q4_xpitch(a.kr);
+  const Q4Smem sm = q4_smem(NR, a.kr, G, a.split);
+  bf16* xs = reinterpret_cast<bf16*>(q4_smem_buf);
+  float* xg = reinterpret_cast<float*>(q4_smem_buf + sm.xg);
+  float* fac = reinterpret_cast<float*>(q4_smem_buf + sm.fac);
+  float4* red = reinterpret_cast<float4*>(q4_smem_buf + sm.red);    // [2][warps][NT][32]
+  float4* part = reinterpret_cast<float4*>(q4_smem_buf + sm.part);  // (split) [tiles][NT][32]
+  const uint32_t ring = smem_u32(q4_smem_buf) + sm.ring + warp * a.ring * SLOT;
+  const uint32_t ring_end = ring + a.ring * SLOT;
   const int ks = a.ks, grp = warp / ks, si = warp % ks, gpb = Q4_WARPS / ks;
   const int ntiles = (a.N + Q4_COLS - 1) / Q4_COLS, nst = (kn + Q4_STAGE - 1) / Q4_STAGE;
+  // pass p of this block: its group's tile is (p gpb + grp) gx + bx, so that
+  // every block has the same number of tiles, give or take one
   const int tstep = gx * gpb;
 
-  // the producer side of this warp's ring
-  int pt = si < nst ? bx * gpb + grp : ntiles, ps = si, pslot = 0;
+  // the producer side of this warp's ring: the next stage's sources (16 bytes
+  // of two rows of nibbles a lane, 16 bytes of scales), its tile and place
+  const int nfull = kn / Q4_STAGE;
+  int pt = si < nst ? grp * gx + bx : ntiles, ps = si;
+  uint32_t pslot = ring;
+  const uint32_t dw = g * RP + 16 * t, dsc = Q4_COLS * RP + lane * 16;
+  const uint8_t *w0 = nullptr, *w1 = nullptr;
+  const bf16* scp = nullptr;
+  bool sc_live = false;
+  auto tile_sources = [&]() {
+    const int n0 = pt * Q4_COLS, kk = k0 + ps * Q4_STAGE;
+    // columns past N read the last one and are dropped
+    w0 = a.W + ((size_t)min(n0 + g, a.N - 1) * a.K + kk) / 2 + 16 * t;
+    w1 = a.W + ((size_t)min(n0 + g + 8, a.N - 1) * a.K + kk) / 2 + 16 * t;
+    // 16 columns of scales a group, 8 a copy (the pitch is a multiple of 8)
+    const int c = n0 + 8 * (lane & 1);
+    sc_live = lane < 2 * GS && c < a.pitch;
+    scp = a.sc + (size_t)(kk / G + (lane >> 1)) * a.pitch + c;
+  };
+  if (pt < ntiles) tile_sources();
+  const size_t sc_step = (size_t)ks * GS * a.pitch;
+  const int w_step = ks * (Q4_STAGE / 2);
   auto issue = [&]() {
     if (pt < ntiles) {
-      const uint32_t dst = ring + pslot * SLOT;
-      const int kk = k0 + ps * Q4_STAGE, nseg = min(Q4_STAGE, k0 + kn - kk) / 32;
-      const int n0 = pt * Q4_COLS;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = (lane >> 2) + 8 * h;
-        const int n = min(n0 + row, a.N - 1);  // columns past N read the last one and are dropped
-        if (t < nseg) cp_async16(dst + row * Q4_ROWPITCH + 16 * t, a.W + ((size_t)n * a.K + kk) / 2 + 16 * t);
-      }
-      // 16 columns of scales a group, 8 a copy (the pitch is a multiple of 8)
-      if (lane < 2 * GS) {
-        const int j = lane >> 1, c = n0 + 8 * (lane & 1);
-        if (kk + j * G < k0 + kn && c < a.pitch)
-          cp_async16(dst + Q4_COLS * Q4_ROWPITCH + lane * 16, a.sc + (size_t)(kk / G + j) * a.pitch + c);
+      if (ps < nfull) {
+        cp_async16(pslot + dw, w0);
+        cp_async16(pslot + dw + 8 * RP, w1);
+        if (sc_live) cp_async16(pslot + dsc, scp);
+      } else {
+        const int left = kn - nfull * Q4_STAGE;  // (a multiple of 32 and of G)
+        if (t < left / 32) {
+          cp_async16(pslot + dw, w0);
+          cp_async16(pslot + dw + 8 * RP, w1);
+        }
+        if (sc_live && (lane >> 1) * G < left) cp_async16(pslot + dsc, scp);
       }
       ps += ks;
+      w0 += w_step;
+      w1 += w_step;
+      scp += sc_step;
       if (ps >= nst) {
         ps = si;
         pt += tstep;
+        if (pt < ntiles) tile_sources();
       }
     }
     cp_commit();
-    pslot = pslot + 1 == a.ring ? 0 : pslot + 1;
+    pslot = pslot + SLOT == ring_end ? ring : pslot + SLOT;
   };
 
   pdl_trigger();
@@ -416,93 +556,116 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
   if (!a.w_early) pdl_wait();
   for (int i = 0; i < a.ring - 1; ++i) issue();
   if (a.w_early) pdl_wait();
-  q4_stage_x<NR>(a, xs, xp, k0, kn, warp, lane);
+  q4_stage_x<NR, G>(a, xs, xp, xg, fac, wmax, k0, kn, warp, lane);
   __syncthreads();
 
   const uint32_t xb = smem_u32(xs) + (uint32_t)(g * xp * 2 + 16 * t);
-  int cslot = 0, par = 0, it = 0;
+  const uint32_t xgb = smem_u32(xg) + (uint32_t)(2 * t * 4);
+  const uint32_t xm = (uint32_t)(8 * xp * 2);
+  uint32_t cslot = ring;
+  float acc[NT][4];
+  // the products of groups [0, ng) of the stage in cslot, stage s of the k range
+  auto stage = [&](int s, int ng) {
+    const uint32_t w = cslot + g * RP + 4 * W * t;
+    const uint32_t sc = cslot + Q4_COLS * RP + 2 * g;
+    const uint32_t xk = xb + s * Q4_STAGE * 2, xgk = xgb + s * GS * NR * 4;
+#pragma unroll
+    for (int j = 0; j < GS; ++j) {
+      if (j < ng) {
+        // a second chain of sums where a lane has several words of a group
+        float c0[NT][4], c1[NT][4];
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          const float2 x8 = lds64f(xgk + (j * NR + 8 * m) * 4);
+          c0[m][0] = c0[m][2] = x8.x;
+          c0[m][1] = c0[m][3] = x8.y;
+          c1[m][0] = c1[m][1] = c1[m][2] = c1[m][3] = 0.f;
+        }
+        uint32_t wa[W], wb[W];
+        lds_words<W>(w + 16 * W * j, wa);
+        lds_words<W>(w + 8 * RP + 16 * W * j, wb);
+#pragma unroll
+        for (int c = 0; c < W; ++c) {
+          constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
+          const uint32_t va = wa[c] >> 8, vb = wb[c] >> 8;
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            const uint4 xv = lds128(xk + m * xm + 64 * (W * j + c));
+            q4_mma(c0[m], wa[c] & LO, wb[c] & LO, wa[c] & HI, wb[c] & HI, xv.x, xv.y);
+            q4_mma(W > 1 ? c1[m] : c0[m], va & LO, vb & LO, va & HI, vb & HI, xv.z, xv.w);
+          }
+        }
+        const float s0 = lds_bf16(sc + 32 * j), s1 = lds_bf16(sc + 32 * j + 16);
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[m][i] = fmaf(i < 2 ? s0 : s1, W > 1 ? c0[m][i] + c1[m][i] : c0[m][i], acc[m][i]);
+      }
+    }
+  };
+  int par = 0, it = 0;
   const int ptg = Q4_PART_TILES / gpb;  // (split) tile passes between exchanges
-  for (int base = bx * gpb; base < ntiles; base += tstep) {
-    const int tile = base + grp;
-    float acc[NT][4];
+  for (int base = bx; base < ntiles; base += tstep) {
+    const int tile = base + grp * gx;
+    const bool joins = si == it % ks;  // the warps of a tile take turns at its epilogue
+    Q4Pre<NT> pre;
+    if (joins && a.split == 1) q4_preload<NT>(a, pre, tile * Q4_COLS, g, t);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
     if (tile < ntiles) {
       for (int s = si; s < nst; s += ks) {
-        cp_wait(a.ring - 2);
+        cp_wait_ring(a.ring);
         __syncwarp();  // every lane's copies of this stage have landed; the slot before it is free
         issue();
-        const uint32_t w = ring + cslot * SLOT + g * Q4_ROWPITCH + 4 * t;
-        const uint32_t sc = ring + cslot * SLOT + Q4_COLS * Q4_ROWPITCH + 2 * g;
-        const int nch = min(Q4_STAGE, kn - s * Q4_STAGE) / 32;
-        const uint32_t xk = xb + s * Q4_STAGE * 2;
-#pragma unroll
-        for (int j = 0; j < GS; ++j) {
-          if (j * CG < nch) {
-            float c0[NT][4], c1[NT][4];
-#pragma unroll
-            for (int m = 0; m < NT; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) c0[m][i] = c1[m][i] = 0.f;
-#pragma unroll
-            for (int ch = j * CG; ch < (j + 1) * CG; ++ch) {
-              const uint32_t wa = lds32(w + 16 * ch), wb = lds32(w + 8 * Q4_ROWPITCH + 16 * ch);
-              const uint32_t p0 = q4_pair(wa, 0), p1 = q4_pair(wb, 0), p2 = q4_pair(wa, 1), p3 = q4_pair(wb, 1);
-              const uint32_t p4 = q4_pair(wa, 2), p5 = q4_pair(wb, 2), p6 = q4_pair(wa, 3), p7 = q4_pair(wb, 3);
-#pragma unroll
-              for (int m = 0; m < NT; ++m) {
-                const uint4 xv = lds128(xk + (uint32_t)(m * 8 * xp * 2) + 64 * ch);
-                q4_mma(c0[m], p0, p1, p2, p3, xv.x, xv.y);
-                q4_mma(c1[m], p4, p5, p6, p7, xv.z, xv.w);
-              }
-            }
-            const float s0 = lds_bf16(sc + 32 * j), s1 = lds_bf16(sc + 32 * j + 16);
-#pragma unroll
-            for (int m = 0; m < NT; ++m) {
-              acc[m][0] = fmaf(s0, c0[m][0] + c1[m][0], acc[m][0]);
-              acc[m][1] = fmaf(s0, c0[m][1] + c1[m][1], acc[m][1]);
-              acc[m][2] = fmaf(s1, c0[m][2] + c1[m][2], acc[m][2]);
-              acc[m][3] = fmaf(s1, c0[m][3] + c1[m][3], acc[m][3]);
-            }
-          }
-        }
-        cslot = cslot + 1 == a.ring ? 0 : cslot + 1;
+        if (s < nfull) stage(s, GS);
+        else stage(s, (kn - nfull * Q4_STAGE) / G);
+        cslot = cslot + SLOT == ring_end ? ring : cslot + SLOT;
       }
     }
+    // the tile's warps meet: two buffers in turn, a buffer is written again
+    // only after the next barrier, which the warp that read it has then reached
+    float4* rb = red + par * (Q4_WARPS * NT * 32);
+    par ^= 1;
     float4 tot[NT];
-#pragma unroll
-    for (int m = 0; m < NT; ++m) tot[m] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
     if (ks > 1) {
-      // two buffers in turn: a buffer is written again only after the next
-      // barrier, which the warp that read it has then reached
-      float4* rb = red + par * (Q4_WARPS * NT * 32);
-      par ^= 1;
 #pragma unroll
-      for (int m = 0; m < NT; ++m) rb[(warp * NT + m) * 32 + lane] = tot[m];
+      for (int m = 0; m < NT; ++m)
+        rb[(warp * NT + m) * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
       asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ks * 32) : "memory");
-      if (si == 0) {
-        for (int x = 1; x < ks; ++x) {
+    }
+    if (joins) {
 #pragma unroll
-          for (int m = 0; m < NT; ++m) {
-            const float4 q = rb[((warp + x) * NT + m) * 32 + lane];
+      for (int m = 0; m < NT; ++m) {
+        if (ks > 1) {
+          tot[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int x = 0; x < ks; ++x) {
+            const float4 q = rb[((grp * ks + x) * NT + m) * 32 + lane];
             tot[m].x += q.x;
             tot[m].y += q.y;
             tot[m].z += q.z;
             tot[m].w += q.w;
           }
+        } else {
+          tot[m] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
         }
+        // out of the row's scaling and the nibbles' 2^-133
+        const float2 fa = *reinterpret_cast<const float2*>(fac + 4 * (8 * m + 2 * t));
+        const float2 fb = *reinterpret_cast<const float2*>(fac + 4 * (8 * m + 2 * t + 1));
+        tot[m].x = tot[m].x * fa.x * fa.y;
+        tot[m].y = tot[m].y * fb.x * fb.y;
+        tot[m].z = tot[m].z * fa.x * fa.y;
+        tot[m].w = tot[m].w * fb.x * fb.y;
+        if (a.split == 1 && tile < ntiles) q4_epilogue<NT>(a, tot[m], pre, m, tile * Q4_COLS, g, t);
       }
     }
-    if (a.split == 1) {
-      if (si == 0 && tile < ntiles)
-#pragma unroll
-        for (int m = 0; m < NT; ++m) q4_epilogue(a, tot[m], tile * Q4_COLS, g, 8 * m + 2 * t);
-    } else {
+    if (a.split > 1) {
       // tiles of this block since the last exchange: slot (pass, group)
       const int pass = it % ptg;
-      if (si == 0)
+      if (joins)
 #pragma unroll
         for (int m = 0; m < NT; ++m) part[((pass * gpb + grp) * NT + m) * 32 + lane] = tot[m];
       const bool last = base + tstep >= ntiles;
@@ -511,8 +674,9 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
         // slot x is finished by rank x % split, one warp a slot
         const int pbase = base - pass * tstep, nslots = (pass + 1) * gpb;
         for (int x = rank + warp * a.split; x < nslots; x += Q4_WARPS * a.split) {
-          const int tl = pbase + (x / gpb) * tstep + x % gpb;
+          const int tl = pbase + x * gx;
           if (tl < ntiles) {
+            q4_preload<NT>(a, pre, tl * Q4_COLS, g, t);
 #pragma unroll
             for (int m = 0; m < NT; ++m) {
               const uint32_t at = smem_u32(part + (x * NT + m) * 32 + lane);
@@ -524,14 +688,14 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
                 sum.z += q.z;
                 sum.w += q.w;
               }
-              q4_epilogue(a, sum, tl * Q4_COLS, g, 8 * m + 2 * t);
+              q4_epilogue<NT>(a, sum, pre, m, tl * Q4_COLS, g, t);
             }
           }
         }
         cluster_sync_all();  // the slots are free again, and no block leaves while another reads it
       }
-      ++it;
     }
+    ++it;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -543,19 +707,19 @@ struct Q4Plan {
   size_t smem;
 };
 bool q4_plan(int rows, int N, int K, int group, bool ln, Q4Plan* p) {
-  const int NR = rows <= 8 ? 8 : 16, NT = NR / 8;
-  const int slot = Q4_COLS * Q4_ROWPITCH + Q4_STAGE / group * Q4_COLS * 2;
+  const int NR = rows <= 8 ? 8 : 16;
+  const int slot = q4_slot(group);
   const int nst = (K + Q4_STAGE - 1) / Q4_STAGE, ntiles = (N + Q4_COLS - 1) / Q4_COLS;
   for (p->split = 1; p->split <= Q4_MAX_SPLIT; p->split *= 2) {
     p->kr = p->split == 1 ? K : (nst + p->split - 1) / p->split * Q4_STAGE;
-    const size_t fixed = (size_t)NR * q4_xpitch(p->kr) * 2 + (size_t)2 * Q4_WARPS * NT * 512 +
-                         (p->split > 1 ? (size_t)Q4_PART_TILES * NT * 512 : 0);
+    if (NR * p->kr > Q4_WARPS * 32 * 8 * Q4_UNITS) continue;  // more than the lanes hold while staging
+    const size_t fixed = q4_smem(NR, p->kr, group, p->split).ring + 256;  // (256: the kernel's static words)
     if (fixed + (size_t)Q4_WARPS * 2 * slot > Q4_SMEM) continue;
     const int ring = (int)((Q4_SMEM - fixed) / ((size_t)Q4_WARPS * slot));
     // a shallow ring starves the stream: split further while that is possible
     if (ring < 4 && p->split < Q4_MAX_SPLIT && !ln) continue;
-    p->ring = ring < Q4_MAX_RING ? ring : Q4_MAX_RING;
-    p->smem = fixed + (size_t)Q4_WARPS * p->ring * slot;
+    p->ring = ring >= 6 ? 6 : (ring >= 4 ? 4 : 2);
+    p->smem = fixed - 256 + (size_t)Q4_WARPS * p->ring * slot;
     break;
   }
   if (p->split > Q4_MAX_SPLIT) return false;
@@ -564,24 +728,24 @@ bool q4_plan(int rows, int N, int K, int group, bool ln, Q4Plan* p) {
   const int st = (p->kr + Q4_STAGE - 1) / Q4_STAGE;
   for (int ks = 1; ks <= Q4_WARPS; ks *= 2) {
     const int gpb = Q4_WARPS / ks;
-    const long passes = (ntiles + (long)slots * gpb - 1) / ((long)slots * gpb);
-    const long cost = passes * ((st + ks - 1) / ks + 2);
+    if (p->split > 1 && gpb > Q4_PART_TILES) continue;
+    const int per_block = (ntiles + slots - 1) / slots, passes = (per_block + gpb - 1) / gpb;
+    const long cost = (long)passes * ((st + ks - 1) / ks + 2);
     if (best < 0 || cost < best) {
       best = cost;
       p->ks = ks;
     }
   }
-  const int gpb = Q4_WARPS / p->ks;
-  int blocks = (ntiles + gpb - 1) / gpb;
-  if (blocks > slots) blocks = slots;
-  p->grid = blocks * p->split;
+  const char* e = getenv("Q4_KS");
+  if (e) p->ks = atoi(e);
+  p->grid = (ntiles < slots ? ntiles : slots) * p->split;
   return true;
 }
 
 template <int NT, int G>
 int q4_launch(Q4Args& a, const Q4Plan& p, cudaStream_t st) {
   CUDA_TRY(once_per_device((const void*)q4_gemv_kernel<NT, G>, [](int) {
-    return cudaFuncSetAttribute(q4_gemv_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4_SMEM);
+    return cudaFuncSetAttribute(q4_gemv_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q4_SMEM - 256);
   }));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -698,7 +862,7 @@ int gpt2_op_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int N, 
   const long pitch = q4_pitch(N);
   const int shift = group == 32 ? 5 : (group == 64 ? 6 : 7);
   const bf16* sc = reinterpret_cast<const bf16*>(scales);
-  const dim3 grid((N + 15) / 16, (K + 255) / 256);
+  const dim3 grid((N + 8 * DQ_ROWS - 1) / (8 * DQ_ROWS), (K + 255) / 256);
   if (out_fp32)
     CUDA_TRY(launch_k(q4_dequantize_kernel<float>, grid, 256, 0, st, packed, sc, pitch, shift, N, K,
                       reinterpret_cast<float*>(out), (long)ldo));

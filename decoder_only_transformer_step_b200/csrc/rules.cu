@@ -14,12 +14,15 @@
 
 namespace {
 
-constexpr int RL_THREADS = 512;
+constexpr int RL_THREADS = 256;
 constexpr int RL_MAX_SPLIT = 8;          // blocks of a row (a cluster)
-constexpr int RL_MAX_SLICE = 49152;      // ids of a block: one counter word each in shared memory
-constexpr int RL_MAX_BIAS = 4096;
-constexpr uint32_t RL_SEEN = 0x80000000u;  // in the history, not among the generated tokens
-constexpr uint32_t RL_BIAS = 0x40000000u;  // has a bias entry; the low 30 bits count
+constexpr int RL_MAX_SLICE = 32768;      // ids of a block: a word each in shared memory, and their list
+constexpr int RL_MAX_BIAS = 4095;
+constexpr int RL_MAX_HISTORY = (1 << 18) - 1;
+// An id's word: bit 31 where it is in the history before gen_start, bits
+// 18..29 the place of its last bias entry (1 ..), bits 0..17 its occurrences
+// among the generated ids.  0: no rule but the mask touches it.
+constexpr uint32_t RL_SEEN = 0x80000000u, RL_COUNT = (1u << 18) - 1;
 
 struct RulesArgs {
   const float* z;
@@ -28,46 +31,39 @@ struct RulesArgs {
   long ldo;
   int V, per, split;  // ids of a block (a multiple of 32), blocks of a row
   gpt2_logit_rules r;
-  int counted, n_bias;
+  int n_bias, list;   // list: room for the ids with a word (COUNTED)
   int32_t* next;
   int32_t* pos;
 };
 
-struct RowRules {
-  float rep, pres, freq;
-};
-DEVI float penalised(float z, uint32_t w, const RowRules& p) {
-  if (w & ~RL_BIAS) {
-    z = z > 0.f ? __fdiv_rn(z, p.rep) : __fmul_rn(z, p.rep);
-    const uint32_t c = w & (RL_BIAS - 1);
-    if (c) {
-      z = __fsub_rn(z, __fmul_rn(p.freq, (float)c));
-      z = __fsub_rn(z, p.pres);
-    }
-  }
-  return z;
-}
-
 // One row's slice of ids.  Bound by the logits' way in and out of HBM at large
 // batches, by latency at small ones, where a cluster of blocks shares the
-// row.  Each block counts the history's tokens of its own slice in shared
-// memory (integer additions: the order of the atomics does not matter), so
-// no counters are kept, zeroed or joined in global memory; the first batch
-// of logits is requested before that.  Ids with a bias entry are left out of
-// the pass and finished by the thread of their last entry.
+// row.  Each block notes its own slice's bias entries and history in shared
+// memory (integer maxima, sums and ors: the order of the atomics does not
+// matter), so nothing is kept, zeroed or joined in global memory; the first
+// batch of logits is requested before that.  The pass over the slice only
+// masks, copies and compares; the few ids with a word (whoever touches a word
+// first lists its id) are left to a second pass with a thread each, since in
+// the first almost every warp would take their path for one lane.
+template <bool COUNTED, bool MASKED>
 __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_constant__ RulesArgs a) {
-  extern __shared__ uint32_t rl_cnt[];  // [per] counters, then [n_bias] bias ids
+  extern __shared__ uint32_t rl_word[];  // [per] words, [n_bias] bias values, [list] ids
   __shared__ float sv[RL_THREADS / 32];
   __shared__ int si[RL_THREADS / 32];
+  __shared__ int listed;
   constexpr int U = 8;  // loads in flight per thread
   const int rank = a.split > 1 ? (int)cluster_ctarank() : 0;
   const int row = blockIdx.x / a.split, tid = threadIdx.x;
   const int v0 = rank * a.per, nv = max(0, min(a.per, a.V - v0));
   const float* z = a.z + (size_t)row * a.ld + v0;
   float* out = a.out + (size_t)row * a.ldo + v0;
+  float* bias = reinterpret_cast<float*>(rl_word + a.per);
+  uint16_t* list = reinterpret_cast<uint16_t*>(bias + a.n_bias);
   pdl_trigger();
-  if (a.counted)
-    for (int i = tid; i < nv; i += RL_THREADS) rl_cnt[i] = 0;
+  if constexpr (COUNTED) {
+    if (tid == 0) listed = 0;
+    for (int i = tid; i < a.per / 4; i += RL_THREADS) reinterpret_cast<uint4*>(rl_word)[i] = make_uint4(0, 0, 0, 0);
+  }
   pdl_wait();
   float x[U];
 #pragma unroll
@@ -75,21 +71,26 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
     const int i = tid + u * RL_THREADS;
     x[u] = i < nv ? z[i] : -INFINITY;
   }
-  RowRules p = {1.f, 0.f, 0.f};
-  if (a.r.repetition) p.rep = a.r.repetition[row];
-  if (a.r.presence) p.pres = a.r.presence[row];
-  if (a.r.frequency) p.freq = a.r.frequency[row];
   int hn = 0;
-  int* bid = reinterpret_cast<int*>(rl_cnt + a.per);
-  if (a.counted) {
+  if constexpr (COUNTED) {
     if (a.r.history) {
       hn = a.r.history_len[row];
       hn = hn < 0 ? 0 : (hn > a.r.history_ld ? a.r.history_ld : hn);
     }
     const int g0 = a.r.gen_start ? a.r.gen_start[row] : 0;
     const int32_t* hist = a.r.history + (size_t)row * a.r.history_ld;
-    const int32_t* ids = a.r.bias_ids + (size_t)row * a.n_bias;
     __syncthreads();
+    if (a.n_bias) {
+      const size_t at = (size_t)row * a.n_bias;
+      for (int e = tid; e < a.n_bias; e += RL_THREADS) {
+        const int id = a.r.bias_ids[at + e] - v0;
+        bias[e] = a.r.bias_values[at + e];
+        // the last entry stays
+        if (id >= 0 && id < nv && atomicMax(&rl_word[id], (uint32_t)(e + 1) << 18) == 0)
+          list[atomicAdd(&listed, 1)] = (uint16_t)id;
+      }
+      __syncthreads();
+    }
     for (int i0 = tid; i0 < hn; i0 += U * RL_THREADS) {
       int id[U];
 #pragma unroll
@@ -99,63 +100,70 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * RL_THREADS;
         if (id[u] >= 0 && id[u] < nv) {  // ids outside the vocabulary are nobody's
-          if (i >= g0) atomicAdd(&rl_cnt[id[u]], 1u);
-          else atomicOr(&rl_cnt[id[u]], RL_SEEN);
+          const uint32_t old = i0 + u * RL_THREADS >= g0 ? atomicAdd(&rl_word[id[u]], 1u) : atomicOr(&rl_word[id[u]], RL_SEEN);
+          if (old == 0) list[atomicAdd(&listed, 1)] = (uint16_t)id[u];
         }
       }
     }
-    for (int e = tid; e < a.n_bias; e += RL_THREADS) {
-      const int id = ids[e] - v0;
-      bid[e] = id;
-      if (id >= 0 && id < nv) atomicOr(&rl_cnt[id], RL_BIAS);
-    }
     __syncthreads();
   }
-  const uint32_t* allowed = a.r.allowed ? a.r.allowed + (size_t)row * a.r.allowed_ld + (v0 >> 5) : nullptr;
+  const uint32_t* allowed = MASKED ? a.r.allowed + (size_t)row * a.r.allowed_ld + (v0 >> 5) : nullptr;
+  const uint32_t bit = 1u << (tid & 31);  // (the stride of a thread's ids is a multiple of 32)
   float bv = -INFINITY;
   int bi = 0x7fffffff;
-  for (int i0 = tid; i0 < nv; i0 += U * RL_THREADS) {
+  auto finish = [&](int i, float t, uint32_t w, uint32_t m) {
+    if (MASKED && !(m & bit)) t = -INFINITY;
+    if (COUNTED && w) return;
+    out[i] = t;
+    if (!(t <= bv) && bv == bv) {  // larger, or the first NaN: a thread meets its ids in rising order
+      bv = t;
+      bi = i;
+    }
+  };
+  int i0 = tid;
+  for (; i0 + (U - 1) * RL_THREADS < nv; i0 += U * RL_THREADS) {
     float y[U];
     uint32_t w[U], m[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * RL_THREADS;
       y[u] = x[u];
-      w[u] = a.counted && i < nv ? rl_cnt[i] : 0u;
-      m[u] = allowed && i < nv ? allowed[i >> 5] : 0xffffffffu;
+      w[u] = COUNTED ? rl_word[i0 + u * RL_THREADS] : 0u;
+      m[u] = MASKED ? allowed[(i0 >> 5) + u * (RL_THREADS / 32)] : 0u;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {  // the next batch
       const int i = i0 + (U + u) * RL_THREADS;
-      x[u] = i < nv ? z[i] : -INFINITY;
+      if (i < nv) x[u] = z[i];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * RL_THREADS;
-      if (i >= nv || (w[u] & RL_BIAS)) continue;
-      const float t = (m[u] >> (i & 31)) & 1u ? penalised(y[u], w[u], p) : -INFINITY;
-      out[i] = t;
-      if (t > bv || (t != t && bv == bv)) {  // a thread meets its ids in rising order
-        bv = t;
-        bi = v0 + i;
-      }
-    }
+    for (int u = 0; u < U; ++u) finish(i0 + u * RL_THREADS, y[u], w[u], m[u]);
   }
-  for (int e = tid; e < a.n_bias; e += RL_THREADS) {
-    const int i = bid[e];
-    if (i < 0 || i >= nv) continue;
-    bool last = true;  // of several entries of an id the last one counts
-    for (int f = e + 1; f < a.n_bias; ++f) last = last && bid[f] != i;
-    if (!last) continue;
-    float t = -INFINITY;
-    if (!allowed || (allowed[i >> 5] >> (i & 31)) & 1u)
-      t = __fadd_rn(penalised(z[i], rl_cnt[i], p), a.r.bias_values[(size_t)row * a.n_bias + e]);
-    out[i] = t;
-    if (greedy_better(t, v0 + i, bv, bi)) {
-      bv = t;
-      bi = v0 + i;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = i0 + u * RL_THREADS;
+    if (i < nv) finish(i, x[u], COUNTED ? rl_word[i] : 0u, MASKED ? allowed[i >> 5] : 0u);
+  }
+  if (bi != 0x7fffffff) bi += v0;
+  if constexpr (COUNTED) {
+    const int n = listed;
+    if (tid < n) {
+      const float rep = a.r.repetition ? a.r.repetition[row] : 1.f, pres = a.r.presence ? a.r.presence[row] : 0.f,
+                  freq = a.r.frequency ? a.r.frequency[row] : 0.f;
+      for (int j = tid; j < n; j += RL_THREADS) {
+        const int i = list[j];
+        const uint32_t w = rl_word[i], c = w & RL_COUNT, e = (w >> 18) & 0xfffu;
+        float t = z[i];
+        if (c || (w & RL_SEEN)) t = t > 0.f ? __fdiv_rn(t, rep) : __fmul_rn(t, rep);
+        if (c) t = __fsub_rn(__fsub_rn(t, __fmul_rn(freq, (float)c)), pres);
+        if (e) t = __fadd_rn(t, bias[e - 1]);
+        if (MASKED && !((allowed[i >> 5] >> (i & 31)) & 1u)) t = -INFINITY;
+        out[i] = t;
+        if (greedy_better(t, v0 + i, bv, bi)) {
+          bv = t;
+          bi = v0 + i;
+        }
+      }
     }
   }
   if (!a.next) return;
@@ -206,6 +214,31 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
   if (a.split > 1) cluster_sync_all();  // no block leaves while rank 0 reads it
 }
 
+template <bool COUNTED, bool MASKED>
+int rules_launch(const RulesArgs& a, int rows, cudaStream_t st) {
+  CUDA_TRY(once_per_device((const void*)logit_rules_kernel<COUNTED, MASKED>, [](int) {
+    return cudaFuncSetAttribute(logit_rules_kernel<COUNTED, MASKED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                227 * 1024 - 256);
+  }));
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * a.split));
+  cfg.blockDim = dim3(RL_THREADS);
+  cfg.dynamicSmemBytes = COUNTED ? (size_t)a.per * 4 + (size_t)a.n_bias * 4 + (size_t)a.list * 2 : 0;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, logit_rules_kernel<COUNTED, MASKED>, a));
+  LAUNCH_CHECK();
+  return GPT2_OK;
+}
+
 bool bad_align(const void* p) { return ((uintptr_t)p & 3) != 0; }
 
 }  // namespace
@@ -223,42 +256,24 @@ int logit_rules(const float* logits, long ld, float* out, long ldo, int rows, in
       bad_align(r->gen_start) || bad_align(r->repetition) || bad_align(r->presence) || bad_align(r->frequency) ||
       bad_align(r->bias_ids) || bad_align(r->bias_values) || bad_align(r->allowed) || bad_align(next) || bad_align(pos))
     return GPT2_ERR_INVALID_ARG;
-  if (vocab > RL_MAX_SPLIT * RL_MAX_SLICE - 32 * RL_MAX_SPLIT || r->n_bias > RL_MAX_BIAS || rows > (1 << 27))
+  if (vocab > RL_MAX_SPLIT * RL_MAX_SLICE || r->n_bias > RL_MAX_BIAS ||
+      (r->history && r->history_ld > RL_MAX_HISTORY) || rows > (1 << 27))
     return GPT2_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0 || vocab == 0) return GPT2_OK;
   RulesArgs a = {};
   a.z = logits; a.ld = ld; a.out = out; a.ldo = ldo; a.V = vocab; a.r = *r; a.next = next; a.pos = pos;
   a.n_bias = r->n_bias;
-  a.counted = r->history || r->n_bias;
   // blocks of a row: 8 while that fits the machine at once, and enough that
-  // the counters of four blocks fit an SM
+  // the words of six blocks fit an SM
   int split = 1;
-  while (split < RL_MAX_SPLIT && ((long)rows * split * 2 <= 4l * num_sms() || (vocab + split - 1) / split > 12800))
+  while (split < RL_MAX_SPLIT && ((long)rows * split * 2 <= 6l * num_sms() || (vocab + split - 1) / split > 8192))
     split *= 2;
   a.split = split;
   a.per = ((vocab + split - 1) / split + 31) / 32 * 32;
-  const size_t smem = a.counted ? (size_t)a.per * 4 + (size_t)a.n_bias * 4 : 0;
-  CUDA_TRY(once_per_device((const void*)logit_rules_kernel, [](int) {
-    return cudaFuncSetAttribute(logit_rules_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (RL_MAX_SLICE + RL_MAX_BIAS) * 4);
-  }));
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * split));
-  cfg.blockDim = dim3(RL_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, logit_rules_kernel, a));
-  LAUNCH_CHECK();
-  return GPT2_OK;
+  const long most = (r->history ? (long)r->history_ld : 0) + r->n_bias;  // ids that can have a word
+  a.list = (int)(most < a.per ? most : a.per);
+  if (most) return a.r.allowed ? rules_launch<true, true>(a, rows, st) : rules_launch<true, false>(a, rows, st);
+  return a.r.allowed ? rules_launch<false, true>(a, rows, st) : rules_launch<false, false>(a, rows, st);
 }
 
 extern "C" {

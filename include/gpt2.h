@@ -352,8 +352,8 @@ typedef struct {
   const int32_t* bias_ids;   /* [rows, n_bias] */
   const float* bias_values;  /* [rows, n_bias] */
   const uint32_t* allowed;   /* [rows, allowed_ld] words: bit v % 32 of word v / 32 set where v is allowed */
-  int history_ld;
-  int n_bias;                /* at most 4096 */
+  int history_ld;            /* at most 262143 */
+  int n_bias;                /* at most 4095 */
   int allowed_ld;            /* at least ceil(vocab / 32) */
   int append;                /* 1: the chosen id is added to history where there is room (history_len + 1) */
 } gpt2_logit_rules;
@@ -560,7 +560,7 @@ int gpt2_op_prefix_attention_bf16(const uint16_t* q, int ldq, const uint16_t* pk
  * v < vocab from logits[r, v] (fp32, row pitches ldo and ld; the same buffer
  * and pitch for an update in place; columns past vocab are left as they were),
  * next[r] (NULL: none) the greedy choice as gpt2_rules_next, pos[r] += 1 (NULL:
- * none; only with next).  vocab at most 392960. */
+ * none; only with next).  vocab at most 262144. */
 int gpt2_op_logit_rules(const float* logits, int ld, float* out, int ldo, int rows, int vocab,
                         const gpt2_logit_rules* rules, int32_t* next, int32_t* pos, void* stream);
 

@@ -86,7 +86,7 @@ def run(z, V, r, ldo=None, in_place=False, **kw):
 
 
 @pytest.mark.parametrize("rows,V,ld", [(1, 1, 1), (3, 31, 40), (2, 513, 513), (5, 5000, 5003), (40, 1000, 1024),
-                                       (150, 777, 777), (300, 300, 301), (1, 200001, 200001), (2, 392960, 392960)])
+                                       (150, 777, 777), (300, 300, 301), (1, 200001, 200001), (2, 262144, 262144)])
 @pytest.mark.parametrize("hist,n_bias,mask", [(0, 0, 1), (1, 1, 0), (90, 40, 1), (3000, 700, 1)])
 def test_rules_bit_by_bit(rows, V, ld, hist, n_bias, mask):
     rng = np.random.default_rng(rows + V + hist)

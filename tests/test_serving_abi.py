@@ -99,8 +99,9 @@ def test_logit_rules_refusals(L):
     assert f(append=1) == f(nxt=None, history=A, history_len=A, history_ld=4, append=1) == INVALID
     assert f(n_bias=3) == f(n_bias=-1) == f(n_bias=2, bias_ids=A) == INVALID
     assert f(allowed=A, allowed_ld=3) == f(presence=A + 2) == f(z=A + 1) == INVALID
-    assert f(n_bias=4097, bias_ids=A, bias_values=A) == SHAPE
-    assert f(V=392961, ld=400000, ldo=400000) == SHAPE
+    assert f(n_bias=4096, bias_ids=A, bias_values=A) == SHAPE
+    assert f(history=A, history_len=A, history_ld=262144) == SHAPE
+    assert f(V=262145, ld=400000, ldo=400000) == SHAPE
     assert f(rows=0) == f(V=0) == 0
 
 
