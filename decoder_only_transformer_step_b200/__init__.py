@@ -411,41 +411,60 @@ def gpt2_op_gemm_bf16_status(A, a_mn, lda, B, b_mn, ldb, C, c_fp32, ldc, M, N, K
 # ---- 4-bit weights, shared prefixes, rules on logits ------------------------
 # These calls know every buffer's extent, so they check it here: a buffer that
 # is too short, of another type or on another device is GPT2_ERR_INVALID_ARG
-# instead of a read out of range.
+# instead of a read out of range.  A decode step makes several of them in a few
+# microseconds of device time, so the checks are kept to what they need.
 
-def _buf(where, name, t, dtypes, need, optional=False):
-    """Address of a device buffer of at least `need` elements (counted along a
-    strided view's last element), or None."""
-    import torch
+_T = None  # what these calls use of torch and of the library, looked up once
+
+
+class _Torch:
+    def __init__(self):
+        import torch
+        self.bf16, self.f32, self.u8, self.i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+        self.words = (torch.int32, torch.uint32)
+        self.current_stream, self.current_device = torch.cuda.current_stream, torch.cuda.current_device
+        lib = _lib()
+        self.quantize, self.dequantize = lib.gpt2_op_q4_quantize, lib.gpt2_op_q4_dequantize
+        self.gemv, self.prefix, self.rules = (lib.gpt2_op_gemv_q4, lib.gpt2_op_prefix_attention_bf16,
+                                              lib.gpt2_op_logit_rules)
+
+
+def _torch():
+    global _T
+    if _T is None:
+        _T = _Torch()
+    return _T
+
+
+def _buf(where, name, t, dtype, dev, need):
+    """Address of a buffer on device `dev` of at least `need` elements (counted
+    up to a strided view's last one); None for None where none are needed."""
     if t is None:
-        if optional or need <= 0:
+        if need <= 0:
             return None
         raise Gpt2Error(-1, f"{where}: {name} is missing")
-    if t.dtype not in dtypes:
-        raise Gpt2Error(-1, f"{where}: {name} is {t.dtype}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.dtype is dtype and t.get_device() == dev and (t.numel() >= need or _span(t) >= need):
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise Gpt2Error(-1, f"{where}: {name} is {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
         raise Gpt2Error(-1, f"{where}: {name} is on {t.device}, not on the current CUDA device")
-    have = t.numel()
-    if have < need and have and not t.is_contiguous():
-        have = 1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
-    if have < need:
-        raise Gpt2Error(-1, f"{where}: {name} holds {have} elements, {need} are needed")
-    return t.data_ptr()
+    raise Gpt2Error(-1, f"{where}: {name} holds {_span(t)} elements, {need} are needed")
 
 
-def _cuda_stream(stream):
-    import torch
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _span(t):
+    return 1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())) if t.numel() else 0
 
 
-def _types():
-    import torch
-    global _BF, _F32, _U8, _I32, _W32
-    _BF, _F32, _U8, _I32 = (torch.bfloat16,), (torch.float32,), (torch.uint8,), (torch.int32,)
-    _W32 = (torch.int32, torch.uint32)
-
-
-_BF = _F32 = _U8 = _I32 = _W32 = None
+def _where(stream, T):
+    """(device index, stream handle) a call runs on."""
+    if stream is None:
+        try:
+            dev = T.current_device()
+        except Exception:  # no GPU: every buffer is on another device
+            return 0, None
+        return dev, T.current_stream(dev).cuda_stream
+    return stream.device_index, stream.cuda_stream
 
 
 def _extent(rows, ld, cols):
@@ -463,35 +482,36 @@ def gpt2_op_q4_scale_count(N, K, group) -> int:
 
 def gpt2_op_q4_quantize(w, w_fp32, ldw, N, K, group, packed, scales, stream=None):
     """w [N, ldw] bf16 (or fp32 with w_fp32) -> packed uint8 [N, K/2], scales bf16 [K/group, N up to a multiple of 8]."""
-    if _BF is None:
-        _types()
-    f = "gpt2_op_q4_quantize"
-    _check(_lib().gpt2_op_q4_quantize(
-        _buf(f, "w", w, _F32 if w_fp32 else _BF, _extent(N, ldw, K)), w_fp32, ldw, N, K, group,
-        _buf(f, "packed", packed, _U8, N * K // 2),
-        _buf(f, "scales", scales, _BF, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), _cuda_stream(stream)), f)
+    T, f = _T or _torch(), "gpt2_op_q4_quantize"
+    dev, st = _where(stream, T)
+    rc = T.quantize(_buf(f, "w", w, T.f32 if w_fp32 else T.bf16, dev, _extent(N, ldw, K)), w_fp32, ldw, N, K, group,
+                    _buf(f, "packed", packed, T.u8, dev, N * K // 2),
+                    _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), st)
+    if rc:
+        raise Gpt2Error(rc, f)
 
 
 def gpt2_op_q4_dequantize(packed, scales, N, K, group, out, out_fp32, ldo, stream=None):
-    if _BF is None:
-        _types()
-    f = "gpt2_op_q4_dequantize"
-    _check(_lib().gpt2_op_q4_dequantize(
-        _buf(f, "packed", packed, _U8, N * K // 2),
-        _buf(f, "scales", scales, _BF, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), N, K, group,
-        _buf(f, "out", out, _F32 if out_fp32 else _BF, _extent(N, ldo, K)), out_fp32, ldo, _cuda_stream(stream)), f)
+    T, f = _T or _torch(), "gpt2_op_q4_dequantize"
+    dev, st = _where(stream, T)
+    rc = T.dequantize(_buf(f, "packed", packed, T.u8, dev, N * K // 2),
+                      _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), N, K,
+                      group, _buf(f, "out", out, T.f32 if out_fp32 else T.bf16, dev, _extent(N, ldo, K)), out_fp32, ldo, st)
+    if rc:
+        raise Gpt2Error(rc, f)
 
 
 def gpt2_op_gemv_q4(x, ldx, packed, scales, bias, out, out_fp32, ldo, rows, N, K, group, stream=None):
     """out [rows, ldo] = x [rows, ldx] W^T (+ bias) with W's 4-bit form; rows 1..16."""
-    if _BF is None:
-        _types()
-    f = "gpt2_op_gemv_q4"
-    _check(_lib().gpt2_op_gemv_q4(
-        _buf(f, "x", x, _BF, _extent(rows, ldx, K)), ldx, _buf(f, "packed", packed, _U8, N * K // 2),
-        _buf(f, "scales", scales, _BF, K // group * ((N + 7) // 8 * 8) if group > 0 else 0),
-        _buf(f, "bias", bias, _BF, N, True), _buf(f, "out", out, _F32 if out_fp32 else _BF, _extent(rows, ldo, N)),
-        out_fp32, ldo, rows, N, K, group, _cuda_stream(stream)), f)
+    T, f = _T or _torch(), "gpt2_op_gemv_q4"
+    dev, st = _where(stream, T)
+    rc = T.gemv(_buf(f, "x", x, T.bf16, dev, _extent(rows, ldx, K)), ldx, _buf(f, "packed", packed, T.u8, dev, N * K // 2),
+                _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0),
+                None if bias is None else _buf(f, "bias", bias, T.bf16, dev, N),
+                _buf(f, "out", out, T.f32 if out_fp32 else T.bf16, dev, _extent(rows, ldo, N)), out_fp32, ldo, rows, N, K,
+                group, st)
+    if rc:
+        raise Gpt2Error(rc, f)
 
 
 def gpt2_op_prefix_attention_scratch_bytes(B, Hq, Hkv, hd, prefix_len, max_len) -> int:
@@ -502,17 +522,19 @@ def gpt2_op_prefix_attention_bf16(q, ldq, pk, pv, prefix_len, prefix_cap, k, v, 
                                   Hkv, hd, stream=None):
     """One token per row over the shared prefix pk, pv [Hkv, prefix_cap, hd] and the rows' own k, v
     [B, Hkv, max_len, hd], of which the first prefix_len and len[b] positions count."""
-    if _BF is None:
-        _types()
-    f = "gpt2_op_prefix_attention_bf16"
+    T, f = _T or _torch(), "gpt2_op_prefix_attention_bf16"
+    dev, st = _where(stream, T)
     np = _extent(Hkv, prefix_cap * hd, prefix_len * hd)
     no = B * Hkv * max_len * hd
-    _check(_lib().gpt2_op_prefix_attention_bf16(
-        _buf(f, "q", q, _BF, _extent(B, ldq, Hq * hd)), ldq, _buf(f, "pk", pk, _BF, np), _buf(f, "pv", pv, _BF, np),
-        prefix_len, prefix_cap, _buf(f, "k", k, _BF, no), _buf(f, "v", v, _BF, no),
-        _buf(f, "len", len, _I32, B if max_len > 0 else 0), max_len, _buf(f, "o", o, _BF, _extent(B, ldo, Hq * hd)), ldo,
-        _buf(f, "lse", lse, _F32, B * Hq, True), _buf(f, "scratch", scratch, _U8, 1), scratch.numel(), B, Hq, Hkv, hd,
-        _cuda_stream(stream)), f)
+    bf = T.bf16
+    rc = T.prefix(_buf(f, "q", q, bf, dev, _extent(B, ldq, Hq * hd)), ldq, _buf(f, "pk", pk, bf, dev, np),
+                  _buf(f, "pv", pv, bf, dev, np), prefix_len, prefix_cap, _buf(f, "k", k, bf, dev, no),
+                  _buf(f, "v", v, bf, dev, no), _buf(f, "len", len, T.i32, dev, B if max_len > 0 else 0), max_len,
+                  _buf(f, "o", o, bf, dev, _extent(B, ldo, Hq * hd)), ldo,
+                  None if lse is None else _buf(f, "lse", lse, T.f32, dev, B * Hq),
+                  _buf(f, "scratch", scratch, T.u8, dev, 1), scratch.numel(), B, Hq, Hkv, hd, st)
+    if rc:
+        raise Gpt2Error(rc, f)
 
 
 class LogitRules:
@@ -527,9 +549,7 @@ class LogitRules:
 
     def __init__(self, history=None, history_len=None, gen_start=None, repetition=None, presence=None, frequency=None,
                  bias_ids=None, bias_values=None, allowed=None, append=False):
-        if _BF is None:
-            _types()
-        f = "LogitRules"
+        T, f = _T or _torch(), "LogitRules"
         per_row = dict(history_len=history_len, gen_start=gen_start, repetition=repetition, presence=presence,
                        frequency=frequency)
         tables = dict(history=history, bias_ids=bias_ids, bias_values=bias_values, allowed=allowed)
@@ -546,35 +566,42 @@ class LogitRules:
         self.rows = rows.pop() if rows else None
         self.tensors = {**per_row, **tables}
         width = {n: 0 if t is None else t.shape[1] for n, t in tables.items()}
+        dev = next((t.get_device() for t in self.tensors.values() if t is not None), 0)
+        if dev < 0:
+            raise Gpt2Error(-1, f"{f}: the rules are not on a CUDA device")
+
+        def at(name, dtype):
+            return _buf(f, name, self.tensors[name], dtype, dev, 0)
+        words = T.words[0] if allowed is None or allowed.dtype is T.words[0] else T.words[1]
+        self.device = dev
         self.c = gpt2_logit_rules(
-            _buf(f, "history", history, _I32, 0), _buf(f, "history_len", history_len, _I32, 0),
-            _buf(f, "gen_start", gen_start, _I32, 0), _buf(f, "repetition", repetition, _F32, 0),
-            _buf(f, "presence", presence, _F32, 0), _buf(f, "frequency", frequency, _F32, 0),
-            _buf(f, "bias_ids", bias_ids, _I32, 0), _buf(f, "bias_values", bias_values, _F32, 0),
-            _buf(f, "allowed", allowed, _W32, 0), width["history"], width["bias_ids"], width["allowed"], int(append))
+            at("history", T.i32), at("history_len", T.i32), at("gen_start", T.i32), at("repetition", T.f32),
+            at("presence", T.f32), at("frequency", T.f32), at("bias_ids", T.i32), at("bias_values", T.f32),
+            at("allowed", words), width["history"], width["bias_ids"], width["allowed"], int(append))
         self._ref = ctypes.byref(self.c)
 
 
-def _rules(where, rules, rows):
-    if rules.rows is not None and rules.rows != rows:
-        raise Gpt2Error(-1, f"{where}: rules for {rules.rows} rows, logits of {rows}")
+def _rules(where, rules, rows, dev):
+    if rules.rows is not None and (rules.rows != rows or rules.device != dev):
+        raise Gpt2Error(-1, f"{where}: rules for {rules.rows} rows on device {rules.device}, logits of {rows} on {dev}")
     return rules._ref
 
 
 def gpt2_op_logit_rules(logits, ld, out, ldo, rows, vocab, rules, next_tokens=None, pos=None, stream=None):
     """out [rows, ldo] = logits [rows, ld] under `rules` (a LogitRules); next_tokens: the greedy choice."""
-    if _BF is None:
-        _types()
-    f = "gpt2_op_logit_rules"
-    _check(_lib().gpt2_op_logit_rules(
-        _buf(f, "logits", logits, _F32, _extent(rows, ld, vocab)), ld, _buf(f, "out", out, _F32, _extent(rows, ldo, vocab)),
-        ldo, rows, vocab, _rules(f, rules, rows), _buf(f, "next_tokens", next_tokens, _I32, rows, True),
-        _buf(f, "pos", pos, _I32, rows, True), _cuda_stream(stream)), f)
+    T, f = _T or _torch(), "gpt2_op_logit_rules"
+    dev, st = _where(stream, T)
+    rc = T.rules(_buf(f, "logits", logits, T.f32, dev, _extent(rows, ld, vocab)), ld,
+                 _buf(f, "out", out, T.f32, dev, _extent(rows, ldo, vocab)), ldo, rows, vocab, _rules(f, rules, rows, dev),
+                 None if next_tokens is None else _buf(f, "next_tokens", next_tokens, T.i32, dev, rows),
+                 None if pos is None else _buf(f, "pos", pos, T.i32, dev, rows), st)
+    if rc:
+        raise Gpt2Error(rc, f)
 
 
 def gpt2_rules_next(ctx, logits, batch, rules, next_tokens, pos=None, stream=None):
     """gpt2_greedy_next under `rules` (a LogitRules); logits are rewritten in place."""
-    _check(_lib().gpt2_rules_next(ctx, _ptr(logits), batch, _rules("gpt2_rules_next", rules, batch), _ptr(next_tokens),
+    _check(_lib().gpt2_rules_next(ctx, _ptr(logits), batch, _rules("gpt2_rules_next", rules, batch, logits.get_device()), _ptr(next_tokens),
                                   _ptr(pos), _stream(stream)), "gpt2_rules_next")
 
 

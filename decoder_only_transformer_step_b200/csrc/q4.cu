@@ -9,8 +9,6 @@
 // Storage: nibbles q + 8, byte j of a row holding k = 2j (low half) and
 // 2j + 1; scales group-major [K / group][pitch], pitch = N rounded up to 8, so
 // that the scales of a tile of output columns are consecutive.
-#include <stdlib.h>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -736,8 +734,6 @@ bool q4_plan(int rows, int N, int K, int group, bool ln, Q4Plan* p) {
       p->ks = ks;
     }
   }
-  const char* e = getenv("Q4_KS");
-  if (e) p->ks = atoi(e);
   p->grid = (ntiles < slots ? ntiles : slots) * p->split;
   return true;
 }

@@ -137,7 +137,10 @@ def test_gemv_against_64_bits(group, rows, N, K):
 
 @pytest.mark.parametrize("N,K,group,rows", [(9, 32, 32, 2), (5, 96, 32, 16), (21, 160, 32, 1), (64, 1600, 64, 16),
                                             (7, 64, 64, 5), (100, 28672, 128, 16), (33, 32768, 32, 16),
-                                            (300, 32768, 64, 8), (5000, 8192, 128, 4), (2000, 20480, 32, 9)])
+                                            (300, 32768, 64, 8), (5000, 8192, 128, 4), (2000, 20480, 32, 9),
+                                            # several tiles a block one after the other
+                                            (40001, 64, 32, 3), (20011, 1600, 64, 12), (30000, 2048, 128, 1),
+                                            (50304, 768, 32, 16), (17000, 12800, 64, 16)])
 def test_gemv_odd_lengths_and_inputs_split_over_a_cluster(N, K, group, rows):
     gemv_case(rows, N, K, group, out32=1, bias=0, seed=N + K)
 
