@@ -18,34 +18,13 @@
 //               to shared memory, then fold O_tile(j-1) into the registers
 // so S(j+1) is computed while the softmax of tile j runs.  Every mbarrier wait
 // is bounded; a timeout sets the device status and the CTA drains and exits.
-#include <cuda.h>
 #include <stdlib.h>
-#include <cudaTypedefs.h>
 
+#include "attention_tc.cuh"
 #include "common.cuh"
 #include "internal.h"
 
 namespace {
-
-// 3-D bf16 tensor map, 128-byte swizzle, box {64, 128, 1}.
-bool tmap_3d(CUtensorMap* tm, const void* base, const uint64_t* dims, const uint64_t* strides,
-             CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, uint32_t box0 = 64, uint32_t box1 = 128) {
-  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  if (!enc) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, s[2] = {strides[0], strides[1]};
-  cuuint32_t box[3] = {box0, box1, 1}, e[3] = {1, 1, 1};
-  return enc(tm, dt, 3, const_cast<void*>(base), d, s, box, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 constexpr int HD = 64, BQ = 128, BKV = 128;
 constexpr int TILE = 128 * 128;  // one 128-row x 64-col bf16 tile, 128B-swizzled
@@ -71,21 +50,6 @@ constexpr int NUM_THREADS = 320;  // TMA warp, MMA warp, 8 softmax warps
 
 #define LN2_F 0.6931471805599453f
 #define LOG2E_F 1.4426950408889634f
-
-DEVI uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// kind::f16 instruction descriptors: fp32 accumulate, bf16 operands, M = 128.
-constexpr uint32_t IDESC_S = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t IDESC_O =
-    (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
 
 DEVI float ex2(float x) {
   float y;
@@ -440,17 +404,6 @@ constexpr float F2_RESCALE = 8.f;  // log2 of the largest un-rescaled probabilit
 constexpr int F2_THREADS = 384;
 constexpr int F2_LAUNCH_REGS = 168, F2_REGS_CTRL = 80, F2_REGS_SOFT = 208;
 static_assert(128 * F2_REGS_CTRL + 256 * F2_REGS_SOFT <= F2_THREADS * F2_LAUNCH_REGS, "register split");
-
-template <int N> DEVI void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> DEVI void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// max(a, b, c): the three-operand form of max.f32 (NaN operands are
-// ignored as by fmaxf), half the instructions of a pairwise row maximum.
-DEVI float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 
 __global__ void __launch_bounds__(F2_THREADS, 1)
     attn_fwd_tc2_kernel(const __grid_constant__ CUtensorMap tmQKV, const __grid_constant__ CUtensorMap tmO,

@@ -1115,7 +1115,8 @@ int gpt2_op_linear_bf16(const uint16_t* x, const uint16_t* w, const uint16_t* bi
 int gpt2_set_wait_timeout_ns(uint64_t ns) {
   const unsigned long long v = ns ? (unsigned long long)ns : WAIT_TIMEOUT_NS;
   TRY(gemm_tc_set_wait_limit(v));
-  return attn_tc_set_wait_limit(v);
+  TRY(attn_tc_set_wait_limit(v));
+  return prefix_set_wait_limit(v);
 }
 
 int gpt2_op_gemm_bf16_status(const uint16_t* A, int a_mn_major, int lda, const uint16_t* B, int b_mn_major, int ldb,

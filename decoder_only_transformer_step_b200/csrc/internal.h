@@ -70,6 +70,7 @@ int num_sms();
 // the current device.
 int gemm_tc_set_wait_limit(unsigned long long ns);
 int attn_tc_set_wait_limit(unsigned long long ns);
+int prefix_set_wait_limit(unsigned long long ns);
 
 // tcgen05 causal attention forward / backward, head_dim 64 (bf16).  The
 // backward expects dvec = rowsum(dO * O) and a zeroed fp32 dq_acc; it writes dK,

@@ -10,6 +10,7 @@
 // keys into parts of a fixed length; a part leaves, per row, its running
 // maximum, sum and weighted values (fp32), and a second kernel joins a row's
 // parts in a fixed order.  Rows without any key get o = 0, lse = -inf.
+#include "attention_tc.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -21,6 +22,9 @@ constexpr int PA_STAGES = 3;     // steps in a warp's ring
 constexpr int PA_ROWS = 16;      // query rows of a block (the mma M)
 constexpr int PA_BLOCKS = 296;   // blocks a call is spread over: 2 for each of 148 SMs
 constexpr int PA_MIN_PART = PA_WARPS * PA_KEYS;
+constexpr int PT_BLOCKS = 148;   // blocks of the tcgen05 kernel: one an SM
+constexpr int PT_MIN_ROWS = 16;  // it is taken above so many query rows of a key/value head
+constexpr int PT_MIN_KEYS = 1024;
 
 struct PrefixArgs {
   const void* q;  // [B, ldq], bf16 or fp32 (rounded to bf16 on load)
@@ -33,8 +37,9 @@ struct PrefixArgs {
   int len_add, max_len;
   int B, Hq, Hkv, G;
   float scale_log2;
-  int L;              // keys of a part
+  int Lp, Lo;         // keys of a part of the prefix / of a row's own keys
   int nsp, nso;       // parts of the prefix, parts of a row's own keys (at most)
+  int tc;             // the prefix's parts are prefix_tc_kernel's
   int mtp, mto;       // 16-row tiles of a key/value head's rows in the prefix / of its group
   float* po;          // [nsp + nso][B * Hq][hd]
   float2* pml;        // [nsp + nso][B * Hq]: maximum (log2 units), sum
@@ -97,7 +102,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
   pdl_wait();
   // which part: those of the prefix first (the tiles of one key range next to
   // each other, for L2), then the rows' own
-  const int np = a.nsp * a.Hkv * a.mtp;
+  const int np = a.tc ? 0 : a.nsp * a.Hkv * a.mtp;
   int x = blockIdx.x, part, h, mt, b0 = 0, n, nrows;
   const bf16 *kb, *vb;
   const bool shared_keys = x < np;
@@ -120,7 +125,8 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
     vb = a.v + ((size_t)b0 * a.Hkv + h) * a.max_len * HD;
     nrows = a.G;
   }
-  const int k0 = part * a.L, k1 = min(n, k0 + a.L);
+  const int L = shared_keys ? a.Lp : a.Lo;
+  const int k0 = part * L, k1 = min(n, k0 + L);
   if (k0 >= k1) return;
   // row i of the tile -> (sequence, query head)
   auto row_of = [&](int i, int* b, int* hq) {
@@ -304,6 +310,284 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
   }
 }
 
+// ------------------------------------------------- many rows: tcgen05 ------
+// The prefix's parts where a key/value head has many query rows: the products
+// S = Q K^T (M 128, N 128) and O += P V on the 5th-generation tensor cores, so
+// that up to 256 rows share one pass over the keys.  One block per (key range,
+// key/value head, row group):
+//   warp 0        TMA: K and V tiles of 128 keys, alternately, through a ring
+//   warps 1, 2    MMA issue of row tile 0 / 1 (warp 1 also owns the TMEM)
+//   warps 4..7    softmax of tile 0, warps 8..11 of tile 1, a thread a row
+// Tensor memory of a tile: S (128 fp32 columns), over which the bf16
+// probabilities P (64 columns) are written once S has been read, and O (hd).
+// A tile's chain S -> softmax -> P V -> next S is serial: at hd 128 it takes
+// about 1700 cycles for 128 keys, whose 64 KB take an SM's share of HBM 2800,
+// and the two tiles' chains run side by side.  A row rescales its O only when
+// its maximum grows by more than 2^8 (the probabilities are formed against the
+// older maximum, exact in the final O / l).  Warps without rows take no part.
+// Every wait is bounded; after one that ran out the part's rows become NaN.
+constexpr float PT_RESCALE = 8.f;
+template <int HD> constexpr int pt_slots() { return HD == 128 ? 5 : 8; }
+template <int HD> constexpr int pt_tile() { return 128 * HD * 2; }  // bytes of a 128-row tile
+template <int HD, int NT> constexpr int pt_tiles() { return (NT + pt_slots<HD>()) * pt_tile<HD>(); }
+template <int HD, int NT> constexpr int pt_bars() { return 2 * pt_slots<HD>() + 5 * NT; }
+template <int HD, int NT> constexpr int pt_smem() { return pt_tiles<HD, NT>() + 1024 + pt_bars<HD, NT>() * 8 + 16; }
+constexpr int PT_REGS_CTRL = 80, PT_REGS_SOFT = 208;
+static_assert(128 * PT_REGS_CTRL + 256 * PT_REGS_SOFT <= 384 * 168, "register split");
+
+// Rows of tile t of a group of n: whole warps, the first tile the larger half.
+__host__ __device__ inline int pt_rows(int n, int nt, int t) {
+  if (nt == 1) return n;
+  const int r0 = min((n + 1) / 2 + 31, n + 31) / 32 * 32;
+  return t == 0 ? min(r0, n) : n - min(r0, n);
+}
+
+template <int HD, int NT, typename QT>
+__global__ void __launch_bounds__(128 + 128 * NT, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ PrefixArgs a) {
+  constexpr int NS = pt_slots<HD>(), TB = pt_tile<HD>(), SUB = 128 * 128;  // SUB: 128 rows x 64 columns, 128B-swizzled
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  const uint32_t bars = base + pt_tiles<HD, NT>();
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + pt_tiles<HD, NT>() + pt_bars<HD, NT>() * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto kv_full = [&](int s) { return bars + 8u * s; };
+  auto kv_empty = [&](int s) { return bars + 8u * (NS + s); };
+  // per tile: 0 q_full, 1 s_full, 2 p_full, 3 pv_done, 4 drain
+  auto tbar = [&](int t, int k) { return bars + 8u * (2 * NS + 5 * t + k); };
+  auto q_tile = [&](int t) { return base + (uint32_t)(t * TB); };
+  auto kv_tile = [&](int s) { return base + (uint32_t)((NT + s) * TB); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (row group fastest: the blocks of one key range next to each other, for L2)
+  const int mg = blockIdx.x % a.mtp, h = blockIdx.x / a.mtp % a.Hkv, part = blockIdx.x / (a.mtp * a.Hkv);
+  const int k0 = part * a.Lp, k1 = min(a.P, k0 + a.Lp), nb = (k1 - k0 + 127) / 128;
+  const int M = a.B * a.G, per = (M + a.mtp - 1) / a.mtp, m0 = mg * per, mrows = min(per, M - m0);  // this group's rows
+  auto rows_of = [&](int t) { return pt_rows(mrows, NT, t); };
+
+  if (threadIdx.x == 0) {
+    int tiles = 0;
+    for (int t = 0; t < NT; ++t) tiles += rows_of(t) > 0;
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), tiles);
+    }
+    for (int t = 0; t < NT; ++t) {
+      const int warps = max(1, (rows_of(t) + 31) / 32);
+      mbar_init(tbar(t, 0), warps);
+      mbar_init(tbar(t, 1), 1);
+      mbar_init(tbar(t, 2), warps);
+      mbar_init(tbar(t, 3), 1);
+      mbar_init(tbar(t, 4), 1);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 256 * NT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_start();
+
+  if (warp < 4) {
+    if constexpr (NT == 2) reg_dealloc<PT_REGS_CTRL>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------- TMA ----
+      // tile 2 j is K of block j, tile 2 j + 1 its V
+      int issued = 0;
+      bool ok = true;
+      for (int i = 0; i < 2 * nb; ++i) {
+        const int s = i % NS;
+        if (i >= NS && !mbar_wait_bounded(kv_empty(s), ((i - NS) / NS) & 1, abort_flag, nullptr)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(kv_full(s), TB);
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(kv_tile(s) + c * SUB, (i & 1) ? &tmV : &tmK, kv_full(s), 64 * c, k0 + (i >> 1) * 128, h);
+        ++issued;
+      }
+      if (!ok)
+        for (int i = issued - NS < 0 ? 0 : issued - NS; i < issued; ++i) mbar_drain_bounded(kv_full(i % NS), (i / NS) & 1);
+    } else if ((warp == 1 || (NT == 2 && warp == 2)) && lane == 0 && rows_of(warp - 1) > 0) {
+      // ------------------------------------------------------------- MMA ----
+      const int t = warp - 1;
+      const uint32_t tS = tmem + 256u * t, tO = tS + 128u;
+      bool ok = mbar_wait_bounded(tbar(t, 0), 0, abort_flag, nullptr), issued = false;
+      for (int j = 0; j < nb && ok; ++j) {
+        int i = 2 * j, s = i % NS;
+        // P V of the block before has read P, over which this S goes
+        if (!mbar_wait_bounded(kv_full(s), (i / NS) & 1, abort_flag, nullptr) ||
+            (j && !mbar_wait_bounded(tbar(t, 3), (j - 1) & 1, abort_flag, nullptr))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = (k >> 2) * SUB + (k & 3) * 32;
+          tc_mma_bf16(tS, sdesc(q_tile(t) + off, 16, 1024), sdesc(kv_tile(s) + off, 16, 1024), IDESC_S, k > 0 ? 1u : 0u);
+        }
+        issued = true;
+        tc_commit(tbar(t, 1));
+        tc_commit(kv_empty(s));
+        i = 2 * j + 1;
+        s = i % NS;
+        if (!mbar_wait_bounded(kv_full(s), (i / NS) & 1, abort_flag, nullptr) ||
+            !mbar_wait_bounded(tbar(t, 2), j & 1, abort_flag, nullptr)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int c = 0; c < HD / 64; ++c)
+            tc_mma_bf16_ts(tO + 64u * c, tS + 8u * k, sdesc(kv_tile(s) + c * SUB + k * 2048, 8192, 1024), IDESC_O,
+                           (j > 0 || k > 0) ? 1u : 0u);
+        tc_commit(tbar(t, 3));
+        tc_commit(kv_empty(s));
+      }
+      if (!ok && issued) {
+        tc_commit(tbar(t, 4));
+        mbar_drain_bounded(tbar(t, 4), 0);
+      }
+    }
+  } else {
+    if constexpr (NT == 2) reg_alloc<PT_REGS_SOFT>();
+    // ----------------------------------------------------------- softmax ----
+    // The lanes of quarter q hold the tile's rows 32 q ..; in tile 1 the
+    // quarters are taken from the other end, so that the warps of two partly
+    // filled tiles share the schedulers evenly.
+    const int t = (warp - 4) >> 2, q = warp & 3, at = q * 32 + lane, lr = (t ? 3 - q : q) * 32 + lane;
+    const int rows = rows_of(t);
+    if ((lr & ~31) < rows) {
+      const bool live = lr < rows;
+      const int m = m0 + (t ? rows_of(0) : 0) + (live ? lr : 0), b = m / a.G, hq = h * a.G + m % a.G;
+      {
+        // this thread's row of Q, K-major and 128-byte swizzled
+        const QT* src = reinterpret_cast<const QT*>(a.q) + (size_t)b * a.ldq + (size_t)hq * HD;
+        const uint32_t row = q_tile(t) + (uint32_t)at * 128u;
+#pragma unroll
+        for (int c = 0; c < HD / 8; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = live ? ld_q2<QT>(src + 8 * c + 2 * e) : 0u;
+          st_shared_v4(row + (c >> 3) * SUB + 16u * (uint32_t)((c & 7) ^ (at & 7)), w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tbar(t, 0));
+      }
+      const uint32_t tS = tmem + ((uint32_t)(q * 32) << 16) + 256u * t, tO = tS + 128u;
+      const float scale = a.scale_log2;
+      float m_use = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nb; ++j) {
+        if (!mbar_wait_bounded(tbar(t, 1), j & 1, abort_flag, nullptr)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32u * c, v[c]);
+        tmem_ld_wait();
+        const int left = k1 - (k0 + 128 * j);  // keys of this block and behind it
+        if (left < 128) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= left) v[c][i] = 0xff800000u;
+        }
+        float mxs[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mxs[i] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mxs[(i >> 1) & 7] = fmax3(mxs[(i >> 1) & 7], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+        const float mx = fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
+                               fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
+        const float m_new = fmaxf(m_use, mx * scale);
+        float alpha = 1.f;
+        bool rescale = false;
+        if (j == 0) {
+          m_use = m_new;
+        } else if (m_new > m_use + PT_RESCALE) {
+          alpha = ex2_approx(m_use - m_new);
+          m_use = m_new;
+          rescale = true;
+        }
+        const float ref = m_use == -INFINITY ? 0.f : m_use;  // (no finite score yet)
+        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(-ref, -ref);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), sc2, nm2);
+            const float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sums[i & 1] = __fadd2_rn(sums[i & 1], pr);
+            pk[i] = pack_bf16x2(pr.x, pr.y);
+          }
+          // (all of this warp's S has been loaded: P goes over it)
+          tmem_st_32x32b_x16(tS + 16u * c, pk);
+        }
+        l = l * alpha + ((sums[0].x + sums[0].y) + (sums[1].x + sums[1].y));
+        // P V of the block before has finished (S was issued after it): rare,
+        // rows whose maximum grew rescale their O
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + 32u * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st_32x32b_x32(tO + 32u * c, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tbar(t, 2));
+      }
+      if (ok) ok = mbar_wait_bounded(tbar(t, 3), (nb - 1) & 1, abort_flag, nullptr);
+      tc_fence_after();
+      const size_t slot = (size_t)part * a.B * a.Hq + (size_t)b * a.Hq + hq;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO + 32u * c, o);
+        tmem_ld_wait();
+        if (live)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(a.po + slot * HD + 32 * c + i) =
+                make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+      }
+      if (live) a.pml[slot] = ok ? make_float2(m_use, l) : make_float2(0.f, __int_as_float(0x7fffffff));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256 * NT);
+  }
+}
+
 // Joins the parts of a row (in the order of the parts): a block a row, its
 // warps take the parts in turn, a lane the same dims of each.
 template <int HD>
@@ -316,7 +600,7 @@ __global__ void __launch_bounds__(128)
   __shared__ float2 sml[4];
   pdl_start();
   const int row = blockIdx.x, b = row / a.Hq, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nown = (own_len(a, b) + a.L - 1) / a.L, n = a.nsp + nown;  // the row's parts: slots 0 .. n - 1
+  const int nown = (own_len(a, b) + a.Lo - 1) / a.Lo, n = a.nsp + nown;  // the row's parts: slots 0 .. n - 1
   const size_t rows = (size_t)a.B * a.Hq;
   float M = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
@@ -421,27 +705,41 @@ __global__ void __launch_bounds__(32)
     if (live) o[(size_t)b * d + h * HD + lane * V + e] = acc[e] * inv;
 }
 
-// The split of a call: parts of L keys, so that about PA_BLOCKS blocks share
-// the keys (the rows' own counted at max_len).  From the sizes alone, not the
-// device: the scratch a caller sizes without one is the scratch a call uses.
+// The split of a call, from the sizes alone, not the device: the scratch a
+// caller sizes without one is the scratch a call uses.
 struct PrefixPlan {
-  int L, nsp, nso, mtp, mto;
+  int tc, Lp, Lo, nsp, nso, mtp, mto;
   size_t rows, po_bytes, bytes;
 };
 bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan* p) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || P < 0 || max_len < 0) return false;
   if (hd != 16 && hd != 64 && hd != 128) return false;
   const int G = Hq / Hkv;
-  p->mtp = (int)(((long)B * G + PA_ROWS - 1) / PA_ROWS);
+  const long M = (long)B * G;
   p->mto = (G + PA_ROWS - 1) / PA_ROWS;
-  const double keys = (double)Hkv * p->mtp * P + (double)B * Hkv * p->mto * max_len;
-  long L = (long)(keys / PA_BLOCKS) + 1;
-  L = (L + PA_MIN_PART - 1) / PA_MIN_PART * PA_MIN_PART;
-  const long longest = P > max_len ? P : max_len;
-  if (L > longest + PA_MIN_PART) L = (longest + PA_MIN_PART) / PA_MIN_PART * PA_MIN_PART;
-  p->L = (int)L;
-  p->nsp = (int)((P + L - 1) / L);
-  p->nso = (int)((max_len + L - 1) / L);
+  const long own_blocks = (long)B * Hkv * p->mto;
+  // parts of at least `least` keys, a multiple of it, so that `blocks` blocks share `keys`
+  auto part = [](double keys, long blocks, long least, long longest) {
+    long L = (long)(keys / blocks) + 1;
+    L = (L + least - 1) / least * least;
+    if (L > longest + least) L = (longest + least) / least * least;
+    return (int)L;
+  };
+  p->tc = hd >= 64 && M > PT_MIN_ROWS && P >= PT_MIN_KEYS;
+  if (p->tc) {
+    const long max_rows = M <= 128 ? 128 : 256;
+    p->mtp = (int)((M + max_rows - 1) / max_rows);
+    long parts = PT_BLOCKS / ((long)Hkv * p->mtp);  // one block an SM
+    if (parts < 1) parts = 1;
+    p->Lp = part((double)P, parts, 128, P);
+    p->Lo = part((double)own_blocks * max_len, PA_BLOCKS, PA_MIN_PART, max_len);
+  } else {
+    p->mtp = (int)((M + PA_ROWS - 1) / PA_ROWS);
+    p->Lp = p->Lo = part((double)Hkv * p->mtp * P + (double)own_blocks * max_len, PA_BLOCKS, PA_MIN_PART,
+                         P > max_len ? P : max_len);
+  }
+  p->nsp = (int)(((long)P + p->Lp - 1) / p->Lp);
+  p->nso = (int)(((long)max_len + p->Lo - 1) / p->Lo);
   p->rows = (size_t)B * Hq;
   p->po_bytes = ((size_t)(p->nsp + p->nso) * p->rows * hd * 4 + 255) & ~(size_t)255;
   p->bytes = p->po_bytes + (((size_t)(p->nsp + p->nso) * p->rows * 8 + 255) & ~(size_t)255);
@@ -449,10 +747,27 @@ bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan*
   return true;
 }
 
+template <int HD, int NT, typename QT>
+int prefix_tc_run(const PrefixArgs& a, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  const uint64_t dims[3] = {HD, (uint64_t)a.P, (uint64_t)a.Hkv};
+  const uint64_t strides[2] = {HD * 2, (uint64_t)a.pcap * HD * 2};
+  if (!tmap_3d(&tk, a.pk, dims, strides) || !tmap_3d(&tv, a.pv, dims, strides)) return GPT2_ERR_CUDA;
+  CUDA_TRY(once_per_device((const void*)prefix_tc_kernel<HD, NT, QT>, [](int) {
+    return cudaFuncSetAttribute(prefix_tc_kernel<HD, NT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                pt_smem<HD, NT>());
+  }));
+  CUDA_TRY(launch_k(prefix_tc_kernel<HD, NT, QT>, dim3((unsigned)(a.nsp * a.Hkv * a.mtp)), 128 + 128 * NT,
+                    (size_t)pt_smem<HD, NT>(), st, tk, tv, a));
+  LAUNCH_CHECK();
+  return GPT2_OK;
+}
+
 template <int HD, typename QT>
 int prefix_run(const PrefixArgs& a, bf16* o, long ldo, float* lse, cudaStream_t st) {
-  const long blocks = (long)a.nsp * a.Hkv * a.mtp + (long)a.nso * a.B * a.Hkv * a.mto;
-  if (blocks > 0x7fffffffl || (long)a.B * a.Hq > 0x7fffffffl) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  const long blocks = (a.tc ? 0 : (long)a.nsp * a.Hkv * a.mtp) + (long)a.nso * a.B * a.Hkv * a.mto;
+  if (blocks > 0x7fffffffl || (long)a.nsp * a.Hkv * a.mtp > 0x7fffffffl || (long)a.B * a.Hq > 0x7fffffffl)
+    return GPT2_ERR_UNSUPPORTED_SHAPE;
   if (blocks) {
     CUDA_TRY(once_per_device((const void*)prefix_part_kernel<HD, QT>, [](int) {
       return cudaFuncSetAttribute(prefix_part_kernel<HD, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -462,6 +777,12 @@ int prefix_run(const PrefixArgs& a, bf16* o, long ldo, float* lse, cudaStream_t 
     CUDA_TRY(launch_k(prefix_part_kernel<HD, QT>, dim3((unsigned)blocks), PA_WARPS * 32,
                       (size_t)(pa_smem<HD>() > merge ? pa_smem<HD>() : merge), st, a));
     LAUNCH_CHECK();
+  }
+  if constexpr (HD >= 64) {
+    if (a.tc) {
+      const int rc = (long)a.B * a.G <= 128 ? prefix_tc_run<HD, 1, QT>(a, st) : prefix_tc_run<HD, 2, QT>(a, st);
+      if (rc != GPT2_OK) return rc;
+    }
   }
   CUDA_TRY(launch_k(prefix_join_kernel<HD>, dim3((unsigned)(a.B * a.Hq)), 128, 0, st, a, o, ldo, lse));
   LAUNCH_CHECK();
@@ -487,7 +808,7 @@ int prefix_attention(const PrefixAttn& c, cudaStream_t st) {
   a.len = c.len; a.len_add = c.len_add; a.max_len = c.max_len;
   a.B = c.B; a.Hq = c.Hq; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv;
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)c.hd);
-  a.L = p.L; a.nsp = p.nsp; a.nso = p.nso; a.mtp = p.mtp; a.mto = p.mto;
+  a.tc = p.tc; a.Lp = p.Lp; a.Lo = p.Lo; a.nsp = p.nsp; a.nso = p.nso; a.mtp = p.mtp; a.mto = p.mto;
   a.po = reinterpret_cast<float*>(c.scratch);
   a.pml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(c.scratch) + p.po_bytes);
   bf16* o = reinterpret_cast<bf16*>(c.o);
@@ -513,6 +834,10 @@ int prefix_attention_f32(const float* q, const float* pk, const float* pv, int P
     return GPT2_ERR_UNSUPPORTED_SHAPE;
   LAUNCH_CHECK();
   return GPT2_OK;
+}
+
+int prefix_set_wait_limit(unsigned long long ns) {
+  return set_unit_wait_limit(ns) == 0 ? GPT2_OK : GPT2_ERR_CUDA;
 }
 
 extern "C" {

@@ -98,6 +98,28 @@ def test_many_rows_and_long_prefixes(B, Hq, Hkv, hd, P, max_len):
     check(s)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv", [(17, 3, 3), (32, 2, 2), (43, 3, 1), (64, 2, 1), (65, 4, 2), (40, 32, 8), (256, 1, 1),
+                                      (129, 4, 2), (100, 8, 1)])
+@pytest.mark.parametrize("P", [1024, 1151, 4000])
+def test_many_rows_on_the_tensor_cores(hd, B, Hq, Hkv, P):
+    # one row tile, two even and uneven ones, several row groups; a last block of keys of any length
+    s = make(B, Hq, Hkv, hd, P, 20, [(b * 7) % 21 for b in range(B)], seed=P + B, cap=P + 5, ldq=Hq * hd + 2, ldo=Hq * hd + 4)
+    s["pk"][:, P:] = float("nan")
+    s["pv"][:, P:] = float("inf")
+    call(s)
+    check(s)
+
+
+def test_maxima_that_keep_growing():
+    # keys ordered so that every block raises the maxima: the running sums are rescaled again and again
+    s = make(40, 4, 1, 128, 3000, 0, [0] * 40, seed=8, q_std=3.0)
+    s["q"] = s["q"].abs()
+    s["pk"] = (s["pk"].abs() * torch.linspace(0.0, 1.5, 3000, device="cuda")[None, :, None]).bfloat16()
+    call(s)
+    check(s)
+
+
 def test_sharp_scores_and_lengths_out_of_range():
     # scores of +-60: one key takes nearly all weight; lengths below 0 and past max_len are clamped
     s = make(4, 4, 4, 64, 257, 40, [-5, 0, 41, 1 << 30], seed=1, q_std=8.0)
