@@ -17,11 +17,13 @@
 namespace {
 
 constexpr int PA_WARPS = 4;      // warps of a block: they share its part's keys
-constexpr int PA_KEYS = 32;      // keys of a warp's step
 constexpr int PA_STAGES = 3;     // steps in a warp's ring
 constexpr int PA_ROWS = 16;      // query rows of a block (the mma M)
 constexpr int PA_BLOCKS = 296;   // blocks a call is spread over: 2 for each of 148 SMs
-constexpr int PA_MIN_PART = PA_WARPS * PA_KEYS;
+template <int HD> constexpr int pa_keys() { return HD == 128 ? 16 : 32; }  // keys of a warp's step
+constexpr int PA_MIN_PART = PA_WARPS * 32;
+constexpr int PA_DIRECT_KEYS = 1024;       // a block takes all keys of its rows up to so many keys a row
+constexpr double PA_DIRECT_BYTES = 8e6;    //   and so many bytes that the whole batch reads that way
 constexpr int PT_BLOCKS = 148;   // blocks of the tcgen05 kernel: one an SM
 constexpr int PT_MIN_ROWS = 16;  // it is taken above so many query rows of a key/value head
 constexpr int PT_MIN_KEYS = 1024;
@@ -39,6 +41,7 @@ struct PrefixArgs {
   float scale_log2;
   int Lp, Lo;         // keys of a part of the prefix / of a row's own keys
   int nsp, nso;       // parts of the prefix, parts of a row's own keys (at most)
+  int direct;         // a block takes all keys of its rows
   int tc;             // the prefix's parts are prefix_tc_kernel's
   int mtp, mto;       // 16-row tiles of a key/value head's rows in the prefix / of its group
   float* po;          // [nsp + nso][B * Hq][hd]
@@ -81,7 +84,10 @@ template <> DEVI uint32_t ld_q2<float>(const float* p) {
   return pack_bf16x2(v.x, v.y);
 }
 
-template <int HD> constexpr int pa_smem() { return PA_WARPS * PA_STAGES * 2 * PA_KEYS * HD * 2; }
+template <int HD> constexpr int pa_smem() {
+  constexpr int ring = PA_WARPS * PA_STAGES * 2 * pa_keys<HD>() * HD * 2, join = PA_WARPS * PA_ROWS * ((HD + 4) * 4 + 8);
+  return ring > join ? ring : join;
+}
 
 // One part of the keys for up to 16 query rows.  Bound by HBM reads of keys
 // and values: 4 hd bytes a key feed 16 rows' products (mma.sync m16n8k16),
@@ -91,9 +97,14 @@ template <int HD> constexpr int pa_smem() { return PA_WARPS * PA_STAGES * 2 * PA
 // warps meet once at the end.  Probabilities are rounded to bf16 for the
 // second product (its operand type; their sum stays fp32 of the unrounded
 // ones): half a step, 2^-8 relative at most, as the output's own rounding.
-template <int HD, typename QT>
-__global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid_constant__ PrefixArgs a) {
+// Where a row has few keys in all and the whole batch reads little (DIRECT), a
+// block takes all keys of its rows instead, those of the prefix and then their
+// own, and writes the output itself.
+template <int HD, typename QT, bool DIRECT>
+__global__ void __launch_bounds__(PA_WARPS * 32)
+    prefix_part_kernel(const __grid_constant__ PrefixArgs a, bf16* __restrict__ out, long ldo, float* __restrict__ lse) {
   extern __shared__ __align__(128) uint8_t pa_smem_buf[];
+  constexpr int PA_KEYS = pa_keys<HD>();
   constexpr int C = HD / 8;                       // 16-byte chunks of a key
   constexpr int SWZ = C < 8 ? C - 1 : 7;          // chunk index ^ (key & SWZ): ldmatrix rows in distinct banks
   constexpr int KB = PA_KEYS * HD * 2;            // bytes of a step's keys (and of its values)
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
   pdl_wait();
   // which part: those of the prefix first (the tiles of one key range next to
   // each other, for L2), then the rows' own
-  const int np = a.tc ? 0 : a.nsp * a.Hkv * a.mtp;
+  const int np = DIRECT || a.tc ? 0 : a.nsp * a.Hkv * a.mtp;
   int x = blockIdx.x, part, h, mt, b0 = 0, n, nrows;
   const bf16 *kb, *vb;
   const bool shared_keys = x < np;
@@ -126,8 +137,8 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
     nrows = a.G;
   }
   const int L = shared_keys ? a.Lp : a.Lo;
-  const int k0 = part * L, k1 = min(n, k0 + L);
-  if (k0 >= k1) return;
+  const int k0 = DIRECT ? 0 : part * L, k1 = DIRECT ? n : min(n, k0 + L);
+  if (!DIRECT && k0 >= k1) return;
   // row i of the tile -> (sequence, query head)
   auto row_of = [&](int i, int* b, int* hq) {
     const int m = mt * PA_ROWS + i;
@@ -136,20 +147,24 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
     return m < nrows;
   };
   const uint32_t ring = smem_u32(pa_smem_buf) + warp * (PA_STAGES * 2 * KB);
-  const int nsteps = (k1 - k0 + PA_KEYS - 1) / PA_KEYS;
+  const int psteps = DIRECT ? (a.P + PA_KEYS - 1) / PA_KEYS : 0;  // (DIRECT) steps of the prefix, before the row's own
+  const int nsteps = psteps + (k1 - k0 + PA_KEYS - 1) / PA_KEYS;
   int ps = warp, pslot = 0;
   auto issue = [&]() {
     if (ps < nsteps) {
-      const int j0 = k0 + ps * PA_KEYS;
+      const bool pre = DIRECT && ps < psteps;
+      const int j0 = pre ? ps * PA_KEYS : k0 + (ps - psteps) * PA_KEYS, end = pre ? a.P : k1;
+      const bf16* ks = pre ? a.pk + (size_t)h * a.pcap * HD : kb;
+      const bf16* vs = pre ? a.pv + (size_t)h * a.pcap * HD : vb;
       const uint32_t dst = ring + pslot * 2 * KB;
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
+      for (int i = 0; i < PA_KEYS * C / 32; ++i) {
         const int e = lane + 32 * i, key = e / C, ch = e % C;
-        const bool live = j0 + key < k1;
-        const size_t at = (size_t)(live ? j0 + key : k0) * HD + ch * 8;
+        const bool live = j0 + key < end;
+        const size_t at = (size_t)(live ? j0 + key : j0) * HD + ch * 8;
         const uint32_t d = dst + key * (HD * 2) + ((ch ^ (key & SWZ)) << 4);
-        cp_async16z(d, kb + at, live);
-        cp_async16z(d + KB, vb + at, live);
+        cp_async16z(d, ks + at, live);
+        cp_async16z(d + KB, vs + at, live);
       }
       ps += PA_WARPS;
     }
@@ -200,7 +215,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
         pa_mma(z[2 * j + 1], qf[c], r[2], r[3]);
       }
     }
-    const int left = k1 - (k0 + s * PA_KEYS);
+    const int left = DIRECT && s < psteps ? a.P - s * PA_KEYS : k1 - (k0 + (s - psteps) * PA_KEYS);
     if (left < PA_KEYS) {
 #pragma unroll
       for (int i = 0; i < PA_KEYS / 8; ++i) {
@@ -304,9 +319,18 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
       v.z = fmaf(f, ow.z, v.z);
       v.w = fmaf(f, ow.w, v.w);
     }
-    const size_t at = (size_t)slot * a.B * a.Hq + (size_t)b * a.Hq + hq;
-    *reinterpret_cast<float4*>(a.po + at * HD + c) = v;
-    if (c == 0) a.pml[at] = make_float2(M, lsum);
+    if constexpr (DIRECT) {
+      const bool any = nsteps > 0;
+      const float inv = any ? 1.f / lsum : 0.f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(out + (size_t)b * ldo + (size_t)hq * HD + c);  // (4-byte aligned)
+      dst[0] = pack_bf16x2(v.x * inv, v.y * inv);
+      dst[1] = pack_bf16x2(v.z * inv, v.w * inv);
+      if (lse && c == 0) lse[(size_t)b * a.Hq + hq] = any ? fmaf(M, 0.6931471805599453f, logf(lsum)) : -INFINITY;
+    } else {
+      const size_t at = (size_t)slot * a.B * a.Hq + (size_t)b * a.Hq + hq;
+      *reinterpret_cast<float4*>(a.po + at * HD + c) = v;
+      if (c == 0) a.pml[at] = make_float2(M, lsum);
+    }
   }
 }
 
@@ -318,11 +342,11 @@ __global__ void __launch_bounds__(PA_WARPS * 32) prefix_part_kernel(const __grid
 //   warp 0        TMA: K and V tiles of 128 keys, alternately, through a ring
 //   warps 1, 2    MMA issue of row tile 0 / 1 (warp 1 also owns the TMEM)
 //   warps 4..7    softmax of tile 0, warps 8..11 of tile 1, a thread a row
-// Tensor memory of a tile: S (128 fp32 columns), over which the bf16
-// probabilities P (64 columns) are written once S has been read, and O (hd).
-// A tile's chain S -> softmax -> P V -> next S is serial: at hd 128 it takes
-// about 1700 cycles for 128 keys, whose 64 KB take an SM's share of HBM 2800,
-// and the two tiles' chains run side by side.  A row rescales its O only when
+// A step is 64 keys.  Tensor memory of a tile: two buffers of S (64 fp32
+// columns), over which the step's bf16 probabilities P (32 columns) are
+// written once S has been read, and O (hd).  S of the next step is issued
+// before P V of this one, so that the softmax never waits for the tensor
+// cores.  A row rescales its O only when
 // its maximum grows by more than 2^8 (the probabilities are formed against the
 // older maximum, exact in the final O / l).  Warps without rows take no part.
 // Every wait is bounded; after one that ran out the part's rows become NaN.
@@ -330,8 +354,13 @@ constexpr float PT_RESCALE = 8.f;
 template <int HD> constexpr int pt_slots() { return HD == 128 ? 5 : 8; }
 template <int HD> constexpr int pt_tile() { return 128 * HD * 2; }  // bytes of a 128-row tile
 template <int HD, int NT> constexpr int pt_tiles() { return (NT + pt_slots<HD>()) * pt_tile<HD>(); }
-template <int HD, int NT> constexpr int pt_bars() { return 2 * pt_slots<HD>() + 5 * NT; }
+template <int HD, int NT> constexpr int pt_bars() { return 2 * pt_slots<HD>() + 7 * NT; }
 template <int HD, int NT> constexpr int pt_smem() { return pt_tiles<HD, NT>() + 1024 + pt_bars<HD, NT>() * 8 + 16; }
+// S: M 128, N 64, both K-major; P V: M 128, N hd, V MN-major (its 64-column halves 16 KB apart)
+constexpr uint32_t PT_IDESC_S = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t pt_idesc_o(int hd) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (((uint32_t)hd >> 3) << 17) | ((128u >> 4) << 24);
+}
 constexpr int PT_REGS_CTRL = 80, PT_REGS_SOFT = 208;
 static_assert(128 * PT_REGS_CTRL + 256 * PT_REGS_SOFT <= 384 * 168, "register split");
 
@@ -356,15 +385,15 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto kv_full = [&](int s) { return bars + 8u * s; };
   auto kv_empty = [&](int s) { return bars + 8u * (NS + s); };
-  // per tile: 0 q_full, 1 s_full, 2 p_full, 3 pv_done, 4 drain
-  auto tbar = [&](int t, int k) { return bars + 8u * (2 * NS + 5 * t + k); };
+  // per tile: 0 q_full, 1 2 s_full, 3 4 p_full (of even and odd steps), 5 pv_done, 6 drain
+  auto tbar = [&](int t, int k) { return bars + 8u * (2 * NS + 7 * t + k); };
   auto q_tile = [&](int t) { return base + (uint32_t)(t * TB); };
   auto kv_tile = [&](int s) { return base + (uint32_t)((NT + s) * TB); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (row group fastest: the blocks of one key range next to each other, for L2)
   const int mg = blockIdx.x % a.mtp, h = blockIdx.x / a.mtp % a.Hkv, part = blockIdx.x / (a.mtp * a.Hkv);
-  const int k0 = part * a.Lp, k1 = min(a.P, k0 + a.Lp), nb = (k1 - k0 + 127) / 128;
+  const int k0 = part * a.Lp, k1 = min(a.P, k0 + a.Lp), nh = (k1 - k0 + 63) / 64, nb = (nh + 1) / 2;
   const int M = a.B * a.G, per = (M + a.mtp - 1) / a.mtp, m0 = mg * per, mrows = min(per, M - m0);  // this group's rows
   auto rows_of = [&](int t) { return pt_rows(mrows, NT, t); };
 
@@ -379,9 +408,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       const int warps = max(1, (rows_of(t) + 31) / 32);
       mbar_init(tbar(t, 0), warps);
       mbar_init(tbar(t, 1), 1);
-      mbar_init(tbar(t, 2), warps);
-      mbar_init(tbar(t, 3), 1);
-      mbar_init(tbar(t, 4), 1);
+      mbar_init(tbar(t, 2), 1);
+      mbar_init(tbar(t, 3), warps);
+      mbar_init(tbar(t, 4), warps);
+      mbar_init(tbar(t, 5), 1);
+      mbar_init(tbar(t, 6), 1);
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -421,43 +452,43 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       const int t = warp - 1;
       const uint32_t tS = tmem + 256u * t, tO = tS + 128u;
       bool ok = mbar_wait_bounded(tbar(t, 0), 0, abort_flag, nullptr), issued = false;
-      for (int j = 0; j < nb && ok; ++j) {
-        int i = 2 * j, s = i % NS;
-        // P V of the block before has read P, over which this S goes
-        if (!mbar_wait_bounded(kv_full(s), (i / NS) & 1, abort_flag, nullptr) ||
-            (j && !mbar_wait_bounded(tbar(t, 3), (j - 1) & 1, abort_flag, nullptr))) {
-          ok = false;
-          break;
-        }
+      auto issue_s = [&](int i) -> bool {
+        const int kt = i & ~1, s = kt % NS;  // (tile 2 j of block j = i / 2)
+        if (!(i & 1) && !mbar_wait_bounded(kv_full(s), (kt / NS) & 1, abort_flag, nullptr)) return false;
+        // P V of the step before last has read the P that this S goes over
+        if (i >= 2 && !mbar_wait_bounded(tbar(t, 5), i & 1, abort_flag, nullptr)) return false;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
           const uint32_t off = (k >> 2) * SUB + (k & 3) * 32;
-          tc_mma_bf16(tS, sdesc(q_tile(t) + off, 16, 1024), sdesc(kv_tile(s) + off, 16, 1024), IDESC_S, k > 0 ? 1u : 0u);
+          tc_mma_bf16(tS + 64u * (i & 1), sdesc(q_tile(t) + off, 16, 1024),
+                      sdesc(kv_tile(s) + off + (i & 1) * 8192, 16, 1024), PT_IDESC_S, k > 0 ? 1u : 0u);
         }
         issued = true;
-        tc_commit(tbar(t, 1));
-        tc_commit(kv_empty(s));
-        i = 2 * j + 1;
-        s = i % NS;
-        if (!mbar_wait_bounded(kv_full(s), (i / NS) & 1, abort_flag, nullptr) ||
-            !mbar_wait_bounded(tbar(t, 2), j & 1, abort_flag, nullptr)) {
+        tc_commit(tbar(t, 1 + (i & 1)));
+        if ((i & 1) || i + 1 == nh) tc_commit(kv_empty(s));
+        return true;
+      };
+      ok = ok && issue_s(0);
+      for (int i = 0; i < nh && ok; ++i) {
+        const int vt = i | 1, s = vt % NS;
+        if ((i + 1 < nh && !issue_s(i + 1)) ||
+            (!(i & 1) && !mbar_wait_bounded(kv_full(s), (vt / NS) & 1, abort_flag, nullptr)) ||
+            !mbar_wait_bounded(tbar(t, 3 + (i & 1)), (i >> 1) & 1, abort_flag, nullptr)) {
           ok = false;
           break;
         }
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int c = 0; c < HD / 64; ++c)
-            tc_mma_bf16_ts(tO + 64u * c, tS + 8u * k, sdesc(kv_tile(s) + c * SUB + k * 2048, 8192, 1024), IDESC_O,
-                           (j > 0 || k > 0) ? 1u : 0u);
-        tc_commit(tbar(t, 3));
-        tc_commit(kv_empty(s));
+        for (int k = 0; k < 4; ++k)
+          tc_mma_bf16_ts(tO, tS + 64u * (i & 1) + 8u * k, sdesc(kv_tile(s) + (4 * (i & 1) + k) * 2048, SUB, 1024),
+                         pt_idesc_o(HD), (i > 0 || k > 0) ? 1u : 0u);
+        tc_commit(tbar(t, 5));
+        if ((i & 1) || i + 1 == nh) tc_commit(kv_empty(s));
       }
       if (!ok && issued) {
-        tc_commit(tbar(t, 4));
-        mbar_drain_bounded(tbar(t, 4), 0);
+        tc_commit(tbar(t, 6));
+        mbar_drain_bounded(tbar(t, 6), 0);
       }
     }
   } else {
@@ -490,38 +521,39 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       const float scale = a.scale_log2;
       float m_use = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < nb; ++j) {
-        if (!mbar_wait_bounded(tbar(t, 1), j & 1, abort_flag, nullptr)) {
+      for (int i = 0; i < nh; ++i) {
+        const uint32_t tSi = tS + 64u * (i & 1);
+        if (!mbar_wait_bounded(tbar(t, 1 + (i & 1)), (i >> 1) & 1, abort_flag, nullptr)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t v[4][32];
+        uint32_t v[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32u * c, v[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32(tSi + 32u * c, v[c]);
         tmem_ld_wait();
-        const int left = k1 - (k0 + 128 * j);  // keys of this block and behind it
-        if (left < 128) {
+        const int left = k1 - (k0 + 64 * i);  // keys of this step and behind it
+        if (left < 64) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= left) v[c][i] = 0xff800000u;
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= left) v[c][e] = 0xff800000u;
         }
         float mxs[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mxs[i] = -INFINITY;
+        for (int e = 0; e < 8; ++e) mxs[e] = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mxs[(i >> 1) & 7] = fmax3(mxs[(i >> 1) & 7], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+          for (int e = 0; e < 32; e += 2)
+            mxs[(e >> 1) & 7] = fmax3(mxs[(e >> 1) & 7], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
         const float mx = fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
                                fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
         const float m_new = fmaxf(m_use, mx * scale);
         float alpha = 1.f;
         bool rescale = false;
-        if (j == 0) {
+        if (i == 0) {
           m_use = m_new;
         } else if (m_new > m_use + PT_RESCALE) {
           alpha = ex2_approx(m_use - m_new);
@@ -532,38 +564,44 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(-ref, -ref);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), sc2, nm2);
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sc2, nm2);
             const float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            sums[i & 1] = __fadd2_rn(sums[i & 1], pr);
-            pk[i] = pack_bf16x2(pr.x, pr.y);
+            sums[e & 1] = __fadd2_rn(sums[e & 1], pr);
+            pk[e] = pack_bf16x2(pr.x, pr.y);
           }
           // (all of this warp's S has been loaded: P goes over it)
-          tmem_st_32x32b_x16(tS + 16u * c, pk);
+          tmem_st_32x32b_x16(tSi + 16u * c, pk);
         }
         l = l * alpha + ((sums[0].x + sums[0].y) + (sums[1].x + sums[1].y));
-        // P V of the block before has finished (S was issued after it): rare,
-        // rows whose maximum grew rescale their O
+        // rare: rows whose maximum grew rescale their O, once the P V before is in it
         if (__any_sync(0xffffffffu, rescale)) {
+          if (!mbar_wait_bounded(tbar(t, 5), (i - 1) & 1, abort_flag, nullptr)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < HD / 32; ++c) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(tO + 32u * c, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
             tmem_st_32x32b_x32(tO + 32u * c, o);
           }
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tbar(t, 2));
+        if (lane == 0) mbar_arrive(tbar(t, 3 + (i & 1)));
       }
-      if (ok) ok = mbar_wait_bounded(tbar(t, 3), (nb - 1) & 1, abort_flag, nullptr);
+      // (the last S implied P V of the step nh - 3; a phase is waited for only once the one before it is known complete)
+      if (ok && nh >= 2) ok = mbar_wait_bounded(tbar(t, 5), (nh - 2) & 1, abort_flag, nullptr);
+      if (ok) ok = mbar_wait_bounded(tbar(t, 5), (nh - 1) & 1, abort_flag, nullptr);
       tc_fence_after();
       const size_t slot = (size_t)part * a.B * a.Hq + (size_t)b * a.Hq + hq;
 #pragma unroll
@@ -595,7 +633,7 @@ __global__ void __launch_bounds__(128)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a, bf16* __restrict__ o, long ldo, float* __restrict__ lse) {
   constexpr int V = HD >= 128 ? 4 : 2;   // dims of a lane
   constexpr int NL = HD / V;             // lanes at work (8 at hd 16)
-  constexpr int U = 4;                   // parts in flight
+  constexpr int U = 8;                   // parts in flight
   __shared__ float so[4][HD];
   __shared__ float2 sml[4];
   pdl_start();
@@ -708,7 +746,7 @@ __global__ void __launch_bounds__(32)
 // The split of a call, from the sizes alone, not the device: the scratch a
 // caller sizes without one is the scratch a call uses.
 struct PrefixPlan {
-  int tc, Lp, Lo, nsp, nso, mtp, mto;
+  int direct, tc, Lp, Lo, nsp, nso, mtp, mto;
   size_t rows, po_bytes, bytes;
 };
 bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan* p) {
@@ -725,7 +763,9 @@ bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan*
     if (L > longest + least) L = (longest + least) / least * least;
     return (int)L;
   };
-  p->tc = hd >= 64 && M > PT_MIN_ROWS && P >= PT_MIN_KEYS;
+  p->direct = (long)P + max_len <= PA_DIRECT_KEYS &&
+              (double)own_blocks * ((double)P + max_len) * hd * 4 <= PA_DIRECT_BYTES;
+  p->tc = !p->direct && hd >= 64 && M > PT_MIN_ROWS && P >= PT_MIN_KEYS;
   if (p->tc) {
     const long max_rows = M <= 128 ? 128 : 256;
     p->mtp = (int)((M + max_rows - 1) / max_rows);
@@ -768,14 +808,23 @@ int prefix_run(const PrefixArgs& a, bf16* o, long ldo, float* lse, cudaStream_t 
   const long blocks = (a.tc ? 0 : (long)a.nsp * a.Hkv * a.mtp) + (long)a.nso * a.B * a.Hkv * a.mto;
   if (blocks > 0x7fffffffl || (long)a.nsp * a.Hkv * a.mtp > 0x7fffffffl || (long)a.B * a.Hq > 0x7fffffffl)
     return GPT2_ERR_UNSUPPORTED_SHAPE;
-  if (blocks) {
-    CUDA_TRY(once_per_device((const void*)prefix_part_kernel<HD, QT>, [](int) {
-      return cudaFuncSetAttribute(prefix_part_kernel<HD, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  pa_smem<HD>() > 49152 ? pa_smem<HD>() : 49152);
+  if (a.direct) {
+    CUDA_TRY(once_per_device((const void*)prefix_part_kernel<HD, QT, true>, [](int) {
+      return cudaFuncSetAttribute(prefix_part_kernel<HD, QT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  pa_smem<HD>());
     }));
-    constexpr int merge = PA_WARPS * PA_ROWS * ((HD + 4) * 4 + 8);
-    CUDA_TRY(launch_k(prefix_part_kernel<HD, QT>, dim3((unsigned)blocks), PA_WARPS * 32,
-                      (size_t)(pa_smem<HD>() > merge ? pa_smem<HD>() : merge), st, a));
+    CUDA_TRY(launch_k(prefix_part_kernel<HD, QT, true>, dim3((unsigned)(a.B * a.Hkv * a.mto)), PA_WARPS * 32,
+                      (size_t)pa_smem<HD>(), st, a, o, ldo, lse));
+    LAUNCH_CHECK();
+    return GPT2_OK;
+  }
+  if (blocks) {
+    CUDA_TRY(once_per_device((const void*)prefix_part_kernel<HD, QT, false>, [](int) {
+      return cudaFuncSetAttribute(prefix_part_kernel<HD, QT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  pa_smem<HD>());
+    }));
+    CUDA_TRY(launch_k(prefix_part_kernel<HD, QT, false>, dim3((unsigned)blocks), PA_WARPS * 32, (size_t)pa_smem<HD>(), st,
+                      a, o, ldo, lse));
     LAUNCH_CHECK();
   }
   if constexpr (HD >= 64) {
@@ -808,7 +857,7 @@ int prefix_attention(const PrefixAttn& c, cudaStream_t st) {
   a.len = c.len; a.len_add = c.len_add; a.max_len = c.max_len;
   a.B = c.B; a.Hq = c.Hq; a.Hkv = c.Hkv; a.G = c.Hq / c.Hkv;
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)c.hd);
-  a.tc = p.tc; a.Lp = p.Lp; a.Lo = p.Lo; a.nsp = p.nsp; a.nso = p.nso; a.mtp = p.mtp; a.mto = p.mto;
+  a.direct = p.direct; a.tc = p.tc; a.Lp = p.Lp; a.Lo = p.Lo; a.nsp = p.nsp; a.nso = p.nso; a.mtp = p.mtp; a.mto = p.mto;
   a.po = reinterpret_cast<float*>(c.scratch);
   a.pml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(c.scratch) + p.po_bytes);
   bf16* o = reinterpret_cast<bf16*>(c.o);

@@ -91,7 +91,9 @@ def test_prefix_attention_against_64_bits(hd, P, B, Hq, Hkv):
 
 @pytest.mark.parametrize("B,Hq,Hkv,hd,P,max_len", [(33, 32, 8, 128, 3000, 40), (64, 8, 1, 64, 2049, 9),
                                                    (200, 4, 4, 64, 511, 33), (2, 64, 1, 128, 5000, 600),
-                                                   (16, 12, 12, 64, 3500, 596), (1, 1, 1, 64, 40000, 1)])
+                                                   (16, 12, 12, 64, 3500, 596), (1, 1, 1, 64, 40000, 1),
+                                                   (5, 6, 3, 16, 3000, 50), (64, 8, 8, 16, 1100, 30), (16, 25, 25, 64, 768, 256),
+                                                   (3, 12, 12, 64, 300, 1024), (8, 4, 4, 128, 200, 1500)])
 def test_many_rows_and_long_prefixes(B, Hq, Hkv, hd, P, max_len):
     s = make(B, Hq, Hkv, hd, P, max_len, [(b * 13) % (max_len + 1) for b in range(B)], seed=B)
     call(s)
