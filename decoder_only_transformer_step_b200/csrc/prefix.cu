@@ -17,9 +17,9 @@
 namespace {
 
 constexpr int PA_WARPS = 4;      // warps of a block: they share its part's keys
-constexpr int PA_STAGES = 3;     // steps in a warp's ring
+constexpr int PA_STAGES = 2;     // steps in a warp's ring
 constexpr int PA_ROWS = 16;      // query rows of a block (the mma M)
-constexpr int PA_BLOCKS = 296;   // blocks a call is spread over: 2 for each of 148 SMs
+constexpr int PA_BLOCKS = 444;   // blocks a call is spread over: 3 for each of 148 SMs
 template <int HD> constexpr int pa_keys() { return HD == 128 ? 16 : 32; }  // keys of a warp's step
 constexpr int PA_MIN_PART = PA_WARPS * 32;
 constexpr int PA_DIRECT_KEYS = 1024;       // a block takes all keys of its rows up to so many keys a row
@@ -31,6 +31,7 @@ constexpr int PT_MIN_KEYS = 1024;
 struct PrefixArgs {
   const void* q;  // [B, ldq], bf16 or fp32 (rounded to bf16 on load)
   long ldq;
+  int q_aligned;  // rows of q at 16-byte boundaries
   const bf16 *pk, *pv;  // [Hkv][pcap][hd]
   int P;
   long pcap;
@@ -84,6 +85,18 @@ template <> DEVI uint32_t ld_q2<float>(const float* p) {
   return pack_bf16x2(v.x, v.y);
 }
 
+// eight elements at a 16-byte boundary
+template <typename QT> DEVI void ld_q8(const QT* p, uint32_t (&w)[4]);
+template <> DEVI void ld_q8<bf16>(const bf16* p, uint32_t (&w)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+}
+template <> DEVI void ld_q8<float>(const float* p, uint32_t (&w)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  w[0] = pack_bf16x2(a.x, a.y); w[1] = pack_bf16x2(a.z, a.w);
+  w[2] = pack_bf16x2(b.x, b.y); w[3] = pack_bf16x2(b.z, b.w);
+}
+
 template <int HD> constexpr int pa_smem() {
   constexpr int ring = PA_WARPS * PA_STAGES * 2 * pa_keys<HD>() * HD * 2, join = PA_WARPS * PA_ROWS * ((HD + 4) * 4 + 8);
   return ring > join ? ring : join;
@@ -92,7 +105,7 @@ template <int HD> constexpr int pa_smem() {
 // One part of the keys for up to 16 query rows.  Bound by HBM reads of keys
 // and values: 4 hd bytes a key feed 16 rows' products (mma.sync m16n8k16),
 // which take a few percent of the tensor cores' time, so each warp streams
-// its own steps of 32 keys through a ring of its own (cp.async, two steps
+// its own steps of 16 or 32 keys through a ring of its own (cp.async, a step
 // ahead) without block-wide waits, with its own running maximum and sum; the
 // warps meet once at the end.  Probabilities are rounded to bf16 for the
 // second product (its operand type; their sum stays fp32 of the unrounded
@@ -506,13 +519,20 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         // this thread's row of Q, K-major and 128-byte swizzled
         const QT* src = reinterpret_cast<const QT*>(a.q) + (size_t)b * a.ldq + (size_t)hq * HD;
         const uint32_t row = q_tile(t) + (uint32_t)at * 128u;
+        uint32_t w[HD / 8][4];
+        if (a.q_aligned) {
 #pragma unroll
-        for (int c = 0; c < HD / 8; ++c) {
-          uint32_t w[4];
+          for (int c = 0; c < HD / 8; ++c) ld_q8<QT>(src + 8 * c, w[c]);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = live ? ld_q2<QT>(src + 8 * c + 2 * e) : 0u;
-          st_shared_v4(row + (c >> 3) * SUB + 16u * (uint32_t)((c & 7) ^ (at & 7)), w[0], w[1], w[2], w[3]);
+          for (int c = 0; c < HD / 8; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[c][e] = ld_q2<QT>(src + 8 * c + 2 * e);
         }
+        // (the lanes without a row hold the group's first: finite, and dropped)
+#pragma unroll
+        for (int c = 0; c < HD / 8; ++c)
+          st_shared_v4(row + (c >> 3) * SUB + 16u * (uint32_t)((c & 7) ^ (at & 7)), w[c][0], w[c][1], w[c][2], w[c][3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(tbar(t, 0));
@@ -850,7 +870,7 @@ int prefix_attention(const PrefixAttn& c, cudaStream_t st) {
   if (!prefix_plan(c.B, c.Hq, c.Hkv, c.hd, c.P, c.max_len, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
   if (c.scratch_bytes < p.bytes) return GPT2_ERR_WORKSPACE;
   PrefixArgs a = {};
-  a.q = c.q; a.ldq = c.ldq;
+  a.q = c.q; a.ldq = c.ldq; a.q_aligned = c.ldq % 8 == 0 && ((uintptr_t)c.q & 15) == 0;
   a.pk = reinterpret_cast<const bf16*>(c.pk); a.pv = reinterpret_cast<const bf16*>(c.pv);
   a.P = c.P; a.pcap = c.pcap;
   a.k = reinterpret_cast<const bf16*>(c.k); a.v = reinterpret_cast<const bf16*>(c.v);

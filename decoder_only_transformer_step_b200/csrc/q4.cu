@@ -30,6 +30,7 @@ constexpr int QZ_ROWS = 32, QZ_K = 256;
 // integers come out of the low bits of w r + 1.5 * 2^23.
 DEVI uint32_t q4_word(const float (&w)[8], float s, float r) {
   constexpr float MAGIC = 12582912.f + 8.f;  // bits 0x4b400008
+  if (s == 0.f) return 0x88888888u;
   float far = 0.f, d[8];
   uint32_t word = 0;
 #pragma unroll
@@ -46,9 +47,38 @@ DEVI uint32_t q4_word(const float (&w)[8], float s, float r) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     if (all || !(d[e] < 0.49999f)) {
-      const int q = s == 0.f ? 0 : __float2int_rn(fminf(fmaxf(rintf(w[e] / s), -7.f), 7.f));
+      const int q = __float2int_rn(fminf(fmaxf(rintf(w[e] / s), -7.f), 7.f));
       word = (word & ~(15u << (4 * e))) | ((uint32_t)(q + 8) << (4 * e));
     }
+  }
+  return word;
+}
+
+// The same for bf16 weights, whose quotients by a bf16 s are either halves
+// exactly or at least 2^-13 from them: the nearest integer of w r is right
+// except at exact halves, where the exact remainder w - s q is s / 2 and the
+// even neighbour is taken.  (About every second warp meets one: no division.)
+DEVI uint32_t q4_word_bf16(const float (&w)[8], float s, float r) {
+  constexpr float MAGIC = 12582912.f + 8.f;
+  const float hs = 0.5f * s;
+  float rem[8];
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 7; e >= 0; --e) {
+    const float t = __fmaf_rn(w[e], r, MAGIC);
+    rem[e] = __fmaf_rn(-s, __fsub_rn(t, MAGIC), w[e]);
+    word = word * 16u + __float_as_uint(t);
+  }
+  word -= 0x4b400000u * 0x11111111u;
+  float far = fmaxf(fabsf(rem[0]), fabsf(rem[1]));
+#pragma unroll
+  for (int e = 2; e < 8; e += 2)
+    asm("max.f32 %0, %0, %1, %2;" : "+f"(far) : "f"(fabsf(rem[e])), "f"(fabsf(rem[e + 1])));
+  if (far == hs) {
+    const uint32_t odd = word;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (fabsf(rem[e]) == hs && (odd & (1u << (4 * e)))) word += rem[e] > 0.f ? 1u << (4 * e) : 0u - (1u << (4 * e));
   }
   return word;
 }
@@ -95,12 +125,14 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int o = LG / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bf16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.f);
+    // (a bf16 over 7 is never within 2^-12 of a bf16 rounding border: the product with 1/7 rounds alike)
+    const bf16 sb = __float2bfloat16_rn(sizeof(T) == 2 ? __uint_as_float(top) * (1.f / 7.f) : __uint_as_float(top) / 7.f);
     const float s = __bfloat162float(sb);
     const int n = n0 + warp * 4 + i;
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
-    const uint32_t word = q4_word(v, s, r);
+    // (a tiny, NaN or infinite s goes the careful way)
+    const uint32_t word = sizeof(T) == 2 && s >= 0x1p-100f && s < 0x1p100f ? q4_word_bf16(v, s, r) : q4_word(v, s, r);
     if (n < N && k < K) *reinterpret_cast<uint32_t*>(packed + ((size_t)n * K + k) / 2) = word;
     if (lane % LG == 0) sm[lane / LG][warp * 4 + i] = sb;
   }
@@ -110,6 +142,16 @@ __global__ void __launch_bounds__(256)
     const int j = i / QZ_ROWS, c = i % QZ_ROWS;
     if (k0 + j * G < K && n0 + c < pitch) scales[(size_t)(k0 / G + j) * pitch + n0 + c] = sm[j][c];
   }
+}
+
+DEVI uint32_t q4_mul2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+DEVI uint32_t q4_sub136(uint32_t a) {
+  const uint32_t c = 0x43084308u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // The values the nibbles stand for, s q (exact in fp32, rounded once to bf16
@@ -125,27 +167,34 @@ __global__ void __launch_bounds__(256)
   const int k = (blockIdx.y * 32 + (threadIdx.x & 31)) * 8;
   if (k >= K) return;
   const int n0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * DQ_ROWS;
+  if (n0 >= N) return;
   uint32_t w[DQ_ROWS];
-  float s[DQ_ROWS];
+  // the eight rows' scales lie side by side (n0 and the pitch are multiples of 8)
+  const uint4 s8 = *reinterpret_cast<const uint4*>(scales + (size_t)(k >> group_shift) * pitch + n0);
 #pragma unroll
-  for (int i = 0; i < DQ_ROWS; ++i) {
-    const int n = min(n0 + i, N - 1);
-    w[i] = *reinterpret_cast<const uint32_t*>(packed + ((size_t)n * K + k) / 2);
-    s[i] = to_f(scales[(size_t)(k >> group_shift) * pitch + n]);
-  }
+  for (int i = 0; i < DQ_ROWS; ++i)
+    w[i] = *reinterpret_cast<const uint32_t*>(packed + ((size_t)min(n0 + i, N - 1) * K + k) / 2);
+  const float s[DQ_ROWS] = {bf16lo(s8.x), bf16hi(s8.x), bf16lo(s8.y), bf16hi(s8.y),
+                            bf16lo(s8.z), bf16hi(s8.z), bf16lo(s8.w), bf16hi(s8.w)};
 #pragma unroll
   for (int i = 0; i < DQ_ROWS; ++i) {
     if (n0 + i >= N) break;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = s[i] * (float)((int)((w[i] >> (4 * e)) & 15u) - 8);
     T* p = out + (size_t)(n0 + i) * ldo + k;
+    // nibbles e and e + 4 as bf16: bits 0x4300 | nibble are 128 + nibble
+    uint32_t q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = q4_sub136((w[i] >> (4 * e)) & 0x000f000fu | 0x43004300u);
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      const uint32_t s2 = __float_as_uint(s[i]) >> 16 | __float_as_uint(s[i]);
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = q4_mul2(q[e], s2);
+      *reinterpret_cast<uint4*>(p) = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                                                __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
     } else {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      *reinterpret_cast<float4*>(p) = make_float4(s[i] * bf16lo(q[0]), s[i] * bf16lo(q[1]), s[i] * bf16lo(q[2]), s[i] * bf16lo(q[3]));
+      *reinterpret_cast<float4*>(p + 4) =
+          make_float4(s[i] * bf16hi(q[0]), s[i] * bf16hi(q[1]), s[i] * bf16hi(q[2]), s[i] * bf16hi(q[3]));
     }
   }
 }

@@ -181,3 +181,18 @@ def test_weights_quantised_just_before_are_the_ones_read():
         gp.gpt2_op_q4_dequantize(packed, scales, N, K, group, deq, 1, K)
         y, mag = x.double() @ deq.double().t(), x.double().abs() @ deq.double().abs().t()
         assert bool(((o.double() - y).abs() <= 80 * 2.0**-23 * mag).all())
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.02, 3e-38, 1e37])
+def test_bf16_weights_at_and_around_halves(scale):
+    # every bf16 significand against every scale significand: quotients at exact halves among them
+    K, group = 256, 32
+    rng = np.random.default_rng(21)
+    w = (rng.integers(-255, 256, size=(4096, K)) / 128.0).astype(np.float32)
+    w[:, ::group] = 7 * (rng.integers(128, 256, size=(4096, K // group)) / 128.0) / 2   # sets the scale
+    t = (torch.from_numpy(w) * scale).bfloat16().cuda()
+    packed, scales = buffers(4096, K, group)
+    gp.gpt2_op_q4_quantize(t, 0, K, 4096, K, group, packed, scales)
+    q, s = reference_quantise(t.float().cpu().numpy(), group)
+    np.testing.assert_array_equal(scales.float().cpu().numpy(), s.T)
+    np.testing.assert_array_equal(unpack(packed), q)
