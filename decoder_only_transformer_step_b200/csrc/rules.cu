@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
   __shared__ float sv[RL_THREADS / 32];
   __shared__ int si[RL_THREADS / 32];
   __shared__ int listed;
+  __shared__ __align__(8) uint64_t best[RL_MAX_SPLIT], arrived;
   constexpr int U = 8;  // loads in flight per thread
   const int rank = a.split > 1 ? (int)cluster_ctarank() : 0;
   const int row = blockIdx.x / a.split, tid = threadIdx.x;
@@ -60,6 +61,15 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
   float* bias = reinterpret_cast<float*>(rl_word + a.per);
   uint16_t* list = reinterpret_cast<uint16_t*>(bias + a.n_bias);
   pdl_trigger();
+  // the row's blocks report to rank 0 (below): its barrier is set up first
+  const bool meets = a.next && a.split > 1;
+  if (meets) {
+    if (rank == 0 && tid == 0) {
+      mbar_init(smem_u32(&arrived), 1);
+      mbar_fence_init();
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
   if constexpr (COUNTED) {
     if (tid == 0) listed = 0;
     for (int i = tid; i < a.per / 4; i += RL_THREADS) reinterpret_cast<uint4*>(rl_word)[i] = make_uint4(0, 0, 0, 0);
@@ -167,6 +177,7 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
     }
   }
   if (!a.next) return;
+  if (meets) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
@@ -187,31 +198,40 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
         bv = sv[k];
         bi = si[k];
       }
-    sv[0] = bv;
-    si[0] = bi;
-  }
-  if (a.split > 1) cluster_sync_all();
-  if (rank == 0 && tid == 0) {
-    for (int k = 1; k < a.split; ++k) {
-      float ov;
-      int oi;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(ov) : "r"(mapa_shared(smem_u32(sv), k)) : "memory");
-      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(oi) : "r"(mapa_shared(smem_u32(si), k)) : "memory");
-      if (greedy_better(ov, oi, bv, bi)) {
-        bv = ov;
-        bi = oi;
+    // Ranks above 0 send (value, id) into rank 0's shared memory, counted on
+    // its barrier: no fence waits for this block's stores to HBM, and the
+    // block may leave.
+    if (rank > 0) {
+      const uint64_t v = (uint64_t)(uint32_t)bi << 32 | __float_as_uint(bv);
+      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                       mapa_shared(smem_u32(&best[rank]), 0)),
+                   "l"(v), "r"(mapa_shared(smem_u32(&arrived), 0))
+                   : "memory");
+    } else {
+      if (a.split > 1) {
+        const uint32_t bar = smem_u32(&arrived);
+        mbar_arrive_expect_tx(bar, 8u * (a.split - 1));
+        mbar_drain_bounded(bar, 0);
+        for (int k = 1; k < a.split; ++k) {
+          const uint64_t v = *reinterpret_cast<volatile uint64_t*>(&best[k]);
+          const float ov = __uint_as_float((uint32_t)v);
+          const int oi = (int)(v >> 32);
+          if (greedy_better(ov, oi, bv, bi)) {
+            bv = ov;
+            bi = oi;
+          }
+        }
+      }
+      const int32_t id = bi < a.V ? bi : 0;  // nothing above -inf: id 0, as gpt2_greedy_next
+      a.next[row] = id;
+      if (a.pos) a.pos[row] += 1;
+      // (every block of the row has read the history before it reported)
+      if (a.r.append && hn < a.r.history_ld) {
+        a.r.history[(size_t)row * a.r.history_ld + hn] = id;
+        a.r.history_len[row] = hn + 1;
       }
     }
-    const int32_t id = bi < a.V ? bi : 0;  // nothing above -inf: id 0, as gpt2_greedy_next
-    a.next[row] = id;
-    if (a.pos) a.pos[row] += 1;
-    // (every block of the row has read the history: they met above)
-    if (a.r.append && hn < a.r.history_ld) {
-      a.r.history[(size_t)row * a.r.history_ld + hn] = id;
-      a.r.history_len[row] = hn + 1;
-    }
   }
-  if (a.split > 1) cluster_sync_all();  // no block leaves while rank 0 reads it
 }
 
 template <bool COUNTED, bool MASKED>
