@@ -422,7 +422,10 @@ class _Torch:
         import torch
         self.bf16, self.f32, self.u8, self.i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
         self.words = (torch.int32, torch.uint32)
-        self.current_stream, self.current_device = torch.cuda.current_stream, torch.cuda.current_device
+        # (the bare handle of the current stream, without a Stream object around it, where this torch has it)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream_of = raw if raw is not None else lambda dev: torch.cuda.current_stream(dev).cuda_stream
+        self.current_device = torch.cuda.current_device
         lib = _lib()
         self.quantize, self.dequantize = lib.gpt2_op_q4_quantize, lib.gpt2_op_q4_dequantize
         self.gemv, self.prefix, self.rules = (lib.gpt2_op_gemv_q4, lib.gpt2_op_prefix_attention_bf16,
@@ -461,9 +464,9 @@ def _where(stream, T):
     if stream is None:
         try:
             dev = T.current_device()
+            return dev, T.stream_of(dev)
         except Exception:  # no GPU: every buffer is on another device
             return 0, None
-        return dev, T.current_stream(dev).cuda_stream
     return stream.device_index, stream.cuda_stream
 
 

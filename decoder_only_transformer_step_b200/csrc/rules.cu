@@ -42,9 +42,9 @@ struct RulesArgs {
 // memory (integer maxima, sums and ors: the order of the atomics does not
 // matter), so nothing is kept, zeroed or joined in global memory; the first
 // batch of logits is requested before that.  The pass over the slice only
-// masks, copies and compares; the few ids with a word (whoever touches a word
-// first lists its id) are left to a second pass with a thread each, since in
-// the first almost every warp would take their path for one lane.
+// masks, copies and compares; the few ids with a word are listed and left to a
+// second pass with a thread each, since in the first almost every warp would
+// take their path for one lane.
 template <bool COUNTED, bool MASKED>
 __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_constant__ RulesArgs a) {
   extern __shared__ uint32_t rl_word[];  // [per] words, [n_bias] bias values, [list] ids
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
   __shared__ int si[RL_THREADS / 32];
   __shared__ int listed;
   __shared__ __align__(8) uint64_t best[RL_MAX_SPLIT], arrived;
-  constexpr int U = 8;  // loads in flight per thread
+  constexpr int U = 8, UH = 8;  // loads of logits / of history in flight per thread
   const int rank = a.split > 1 ? (int)cluster_ctarank() : 0;
   const int row = blockIdx.x / a.split, tid = threadIdx.x;
   const int v0 = rank * a.per, nv = max(0, min(a.per, a.V - v0));
@@ -75,44 +75,62 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
     for (int i = tid; i < a.per / 4; i += RL_THREADS) reinterpret_cast<uint4*>(rl_word)[i] = make_uint4(0, 0, 0, 0);
   }
   pdl_wait();
+  // every first load is requested here, so that the phases below wait for HBM
+  // once: the row's lengths, its first history and bias entry, its logits
+  int hn = 0, g0 = 0, be = -1, h0[UH];
+  float bval = 0.f;
+  const size_t brow = (size_t)row * a.n_bias;
+  const int32_t* hist = a.r.history + (size_t)row * a.r.history_ld;
+  if constexpr (COUNTED) {
+    if (a.r.history) hn = a.r.history_len[row];
+    if (a.r.gen_start) g0 = a.r.gen_start[row];
+#pragma unroll
+    for (int u = 0; u < UH; ++u) {
+      const int i = tid + u * RL_THREADS;
+      h0[u] = a.r.history && i < a.r.history_ld ? hist[i] : -1;
+    }
+    if (tid < a.n_bias) {
+      be = a.r.bias_ids[brow + tid];
+      bval = a.r.bias_values[brow + tid];
+    }
+  }
   float x[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int i = tid + u * RL_THREADS;
     x[u] = i < nv ? z[i] : -INFINITY;
   }
-  int hn = 0;
   if constexpr (COUNTED) {
-    if (a.r.history) {
-      hn = a.r.history_len[row];
-      hn = hn < 0 ? 0 : (hn > a.r.history_ld ? a.r.history_ld : hn);
-    }
-    const int g0 = a.r.gen_start ? a.r.gen_start[row] : 0;
-    const int32_t* hist = a.r.history + (size_t)row * a.r.history_ld;
+    hn = a.r.history ? (hn < 0 ? 0 : (hn > a.r.history_ld ? a.r.history_ld : hn)) : 0;
     __syncthreads();
     if (a.n_bias) {
-      const size_t at = (size_t)row * a.n_bias;
       for (int e = tid; e < a.n_bias; e += RL_THREADS) {
-        const int id = a.r.bias_ids[at + e] - v0;
-        bias[e] = a.r.bias_values[at + e];
+        if (e != tid) {
+          be = a.r.bias_ids[brow + e];
+          bval = a.r.bias_values[brow + e];
+        }
+        const int id = be - v0;
+        bias[e] = bval;
         // the last entry stays
         if (id >= 0 && id < nv && atomicMax(&rl_word[id], (uint32_t)(e + 1) << 18) == 0)
           list[atomicAdd(&listed, 1)] = (uint16_t)id;
       }
       __syncthreads();
     }
-    for (int i0 = tid; i0 < hn; i0 += U * RL_THREADS) {
-      int id[U];
+    for (int i0 = tid; i0 < hn; i0 += UH * RL_THREADS) {
+      if (i0 != tid) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * RL_THREADS;
-        id[u] = i < hn ? hist[i] - v0 : -1;
+        for (int u = 0; u < UH; ++u) {
+          const int i = i0 + u * RL_THREADS;
+          h0[u] = i < hn ? hist[i] : -1;
+        }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (id[u] >= 0 && id[u] < nv) {  // ids outside the vocabulary are nobody's
-          const uint32_t old = i0 + u * RL_THREADS >= g0 ? atomicAdd(&rl_word[id[u]], 1u) : atomicOr(&rl_word[id[u]], RL_SEEN);
-          if (old == 0) list[atomicAdd(&listed, 1)] = (uint16_t)id[u];
+      for (int u = 0; u < UH; ++u) {
+        const int i = i0 + u * RL_THREADS, id = h0[u] - v0;
+        if (i < hn && id >= 0 && id < nv) {  // (ids outside the vocabulary are nobody's)
+          const uint32_t old = i >= g0 ? atomicAdd(&rl_word[id], 1u) : atomicOr(&rl_word[id], RL_SEEN);
+          if (old == 0) list[atomicAdd(&listed, 1)] = (uint16_t)id;
         }
       }
     }
