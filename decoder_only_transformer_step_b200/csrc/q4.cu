@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(256)
 // numbers and the lowest normal ones lie on one line), which mma takes
 // exactly, so that one AND leaves two operands (a nibble in the upper half of
 // a byte counts 16-fold).  To match, each row of x is staged times the power
-// of two that brings its largest magnitude to 2^110, a sixteenth of that at
-// odd k: exact in bf16, but for numbers below 2^-230 of the row's largest.
+// of two that brings its largest magnitude to 2^60, a sixteenth of that at
+// odd k: exact in bf16, but for numbers below 2^-180 of the row's largest.
 // The nibbles are q + 8, so a group's sum starts at -8 sum x instead of 0 (the
 // group sums of x are formed once, when x is staged).  A group's products are
 // summed in fp32 by the tensor core and multiplied by the group's scale in
@@ -230,11 +230,11 @@ __global__ void __launch_bounds__(256)
 // meet through distributed shared memory, again in a fixed order.
 constexpr int Q4_WARPS = 16;
 constexpr int Q4_COLS = 16;                    // output columns of a tile (the mma M)
-constexpr int Q4_STAGE = 128;                  // inputs of a stage
+constexpr int Q4_STAGE = 256;                  // inputs of a stage
+constexpr int Q4_RP = Q4_STAGE / 2;            // bytes of a staged row
 constexpr int Q4_MAX_SPLIT = 8;
-constexpr int Q4_PART_TILES = 8;               // tiles whose sums a cluster exchanges at once
+constexpr int Q4_PART_TILES = 8;               // tiles whose sums a cluster exchanges at once (1 where that does not fit)
 constexpr int Q4_MAX_K = 32768;                // widest input
-constexpr int Q4_UNITS = 16;                   // 8-input units of x a lane holds while staging
 constexpr int Q4_SMEM = 227 * 1024;
 
 struct Q4Args {
@@ -251,7 +251,7 @@ struct Q4Args {
   long ldo;
   int epi;           // Q4Epi
   int rows, N, K;
-  int ks, split, kr, ring, w_early;
+  int ks, split, kr, ring, part, w_early, wpr;  // wpr: warps of a row of x while it is staged
   void* kc;
   void* vc;
   const int32_t* pos;
@@ -260,23 +260,25 @@ struct Q4Args {
 enum Q4Epi : int { Q4_BF16 = 0, Q4_F32, Q4_QKV, Q4_RESID, Q4_GELU };
 
 // Shared memory of a block, in bytes: the rows of x, the group sums, the row
-// factors, the warps' sums (two buffers), the cluster's, the rings.
+// factors, the warps' sums, the cluster's, the rings.
 __host__ __device__ inline int q4_xpitch(int kr) { return kr % 64 ? kr : kr + 32; }  // an odd multiple of 64 bytes
-// bytes of a staged row of nibbles: the pitch that spreads the lanes' 16-, 8- or 4-byte reads over all banks
-__host__ __device__ constexpr int q4_rowpitch(int group) { return group == 128 ? 64 : (group == 64 ? 96 : 80); }
-__host__ __device__ constexpr int q4_slot(int group) {
-  return Q4_COLS * q4_rowpitch(group) + Q4_STAGE / group * Q4_COLS * 2;
+__host__ __device__ constexpr int q4_slot(int group) { return Q4_COLS * Q4_RP + Q4_STAGE / group * Q4_COLS * 2; }
+// Where 16-byte piece c of staged row r lies: the pieces are exchanged so that
+// the lanes' 16-, 8- or 4-byte reads of 2, 4 or 8 rows fall into different banks.
+template <int G> DEVI int q4_piece(int r, int c) {
+  constexpr int W = G / 32;
+  return c ^ ((r & (8 / W - 1)) * W);
 }
 struct Q4Smem {
   int xg, fac, red, part, ring;
 };
-__host__ __device__ inline Q4Smem q4_smem(int nr, int kr, int group, int split) {
+__host__ __device__ inline Q4Smem q4_smem(int nr, int rows, int kr, int group, int part_tiles) {
   Q4Smem m;
-  m.xg = nr * q4_xpitch(kr) * 2;
+  m.xg = rows * q4_xpitch(kr) * 2;
   m.fac = m.xg + ((kr / group * nr * 4 + 15) & ~15);
-  m.red = m.fac + 16 * 16;
-  m.part = m.red + 2 * Q4_WARPS * (nr / 8) * 512;
-  m.ring = m.part + (split > 1 ? Q4_PART_TILES * (nr / 8) * 512 : 0);
+  m.red = m.fac + 16 * 8;
+  m.part = m.red + Q4_WARPS * (nr / 8) * 512;
+  m.ring = m.part + part_tiles * (nr / 8) * 512;
   return m;
 }
 
@@ -284,10 +286,10 @@ DEVI void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 DEVI void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest ring - 2 groups have landed (rings of 2, 4 and 6 slots).
+// All but the newest ring - 2 groups have landed (rings of 2, 3 and 4 slots).
 DEVI void cp_wait_ring(int ring) {
-  if (ring == 6) asm volatile("cp.async.wait_group 4;" ::: "memory");
-  else if (ring == 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  if (ring == 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (ring == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 // a lane's W words of a group (W 4, 2 or 1)
@@ -342,128 +344,108 @@ DEVI uint4 q4_pack8(const float4& a, const float4& b) {
   return make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
 }
 
-// Inputs [k0, k0 + kn) of the rows -> xs [NR][xp], their group sums xg
-// [group][NR] and the rows' factors (both 16-byte slots of fac hold two
-// powers of two whose product undoes the row's scaling and the 2^-133).  One
-// or two warps a row; a lane holds its units (8 inputs, as bf16) in registers
-// from the load to the scaled store.
-template <int NR, int G>
-DEVI void q4_stage_x(const Q4Args& a, bf16* xs, int xp, float* xg, float* fac, uint32_t* wmax, int k0, int kn, int warp,
-                     int lane) {
-  constexpr int WPR = Q4_WARPS / NR;  // warps of a row
-  const int r = warp / WPR, part = warp % WPR, n8 = kn / 8;
-  uint4 v[Q4_UNITS];
-#pragma unroll
-  for (int u = 0; u < Q4_UNITS; ++u) v[u] = make_uint4(0u, 0u, 0u, 0u);
-  if (r < a.rows) {
-    if (a.ln) {
-      // (K <= 2048, never split: k0 = 0, kn = K.)  Every warp of the row
-      // holds all of it for the two statistics, and keeps its own part.
-      constexpr int U = 8;
-      const float* src = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi;
-      float4 f[U][2];
-      float s = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = lane + 32 * u;
-        f[u][0] = f[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n8) {
-          f[u][0] = *reinterpret_cast<const float4*>(src + 8 * i);
-          f[u][1] = *reinterpret_cast<const float4*>(src + 8 * i + 4);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        s += ((f[u][0].x + f[u][0].y) + (f[u][0].z + f[u][0].w)) + ((f[u][1].x + f[u][1].y) + (f[u][1].z + f[u][1].w));
-      const float mu = warp_sum(s) / a.K;
-      float q = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (lane + 32 * u < n8) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float t0 = f[u][h].x - mu, t1 = f[u][h].y - mu, t2 = f[u][h].z - mu, t3 = f[u][h].w - mu;
-            q += (t0 * t0 + t1 * t1) + (t2 * t2 + t3 * t3);
-          }
-        }
-      }
-      const float rs = rsqrtf(warp_sum(q) / a.K + 1e-5f);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = lane + 32 * u;
-        if (i < n8 && u % WPR == part) {
-          float4 o[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 gg = q4_ld4(a.ln_g + 8 * i + 4 * h), bb = q4_ld4(a.ln_b + 8 * i + 4 * h);
-            o[h] = make_float4((f[u][h].x - mu) * rs * gg.x + bb.x, (f[u][h].y - mu) * rs * gg.y + bb.y,
-                               (f[u][h].z - mu) * rs * gg.z + bb.z, (f[u][h].w - mu) * rs * gg.w + bb.w);
-          }
-          v[u / WPR] = q4_pack8(o[0], o[1]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < Q4_UNITS; ++u) {
-        const int i = lane + 32 * (u * WPR + part);
-        if (i < n8) {
-          if (a.in_f32) {
-            const float* p = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi + k0 + 8 * i;
-            v[u] = q4_pack8(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4));
-          } else {
-            v[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.in) + (size_t)r * a.ldi + k0 + 8 * i);
-          }
-        }
-      }
+DEVI uint32_t q4_max2(uint32_t m, const uint4& v) {
+  return __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+}
+
+// Inputs [k0, k0 + kn) of the rows -> xs [rows][xp] and the rows' factors
+// (the power of two that undoes the scaling and the 2^-133, as two floats).
+// wpr warps share a row (their number a power of two, the rows' times it at
+// most 16); a lane holds its units of 8 inputs in registers from the load to
+// the scaled store.  Rows past a.rows are not written: what the mma make of
+// them stays in columns that are dropped.  All threads call it.
+template <int G>
+DEVI void q4_stage_x(const Q4Args& a, bf16* xs, int xp, float2* fac, uint32_t* wmax, int k0, int kn, int warp, int lane) {
+  constexpr int U = 8;  // units a lane holds at once
+  constexpr int W = G / 32;
+  const int wpr = a.wpr, r = warp / wpr, part = warp % wpr, n8 = kn / 8, mine = (n8 + wpr - 1 - part) / wpr;
+  // (unit j of this warp's lane: part + wpr * (lane + 32 u))
+  const bool live = r < a.rows;
+  uint4 v[U];
+  float mu = 0.f, rs = 0.f;
+  if (a.ln && live) {
+    // (K <= 2048, one chunk.)  Every warp of the row forms its two statistics.
+    const float* src = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi;
+    float s = 0.f, q = 0.f;
+#pragma unroll 8
+    for (int i = lane; i < 2 * n8; i += 32) {
+      const float4 f = *reinterpret_cast<const float4*>(src + 4 * i);
+      s += (f.x + f.y) + (f.z + f.w);
     }
+    mu = warp_sum(s) / a.K;
+#pragma unroll 8
+    for (int i = lane; i < 2 * n8; i += 32) {
+      const float4 f = *reinterpret_cast<const float4*>(src + 4 * i);
+      const float t0 = f.x - mu, t1 = f.y - mu, t2 = f.z - mu, t3 = f.w - mu;
+      q += (t0 * t0 + t1 * t1) + (t2 * t2 + t3 * t3);
+    }
+    rs = rsqrtf(warp_sum(q) / a.K + 1e-5f);
   }
+  auto load = [&](int j) -> uint4 {
+    const int k = k0 + 8 * (part + wpr * j);
+    if (a.ln) {
+      const float* p = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi + k;
+      float4 o[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = *reinterpret_cast<const float4*>(p + 4 * h);
+        const float4 gg = q4_ld4(a.ln_g + k + 4 * h), bb = q4_ld4(a.ln_b + k + 4 * h);
+        o[h] = make_float4((x.x - mu) * rs * gg.x + bb.x, (x.y - mu) * rs * gg.y + bb.y, (x.z - mu) * rs * gg.z + bb.z,
+                           (x.w - mu) * rs * gg.w + bb.w);
+      }
+      return q4_pack8(o[0], o[1]);
+    }
+    if (a.in_f32) {
+      const float* p = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi + k;
+      return q4_pack8(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4));
+    }
+    return *reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.in) + (size_t)r * a.ldi + k);
+  };
   // the row's largest magnitude, as the bits of a bf16
   uint32_t m2 = 0;
+  if (live) {
 #pragma unroll
-  for (int u = 0; u < Q4_UNITS; ++u)
-    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu),
-                               __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu)));
+    for (int u = 0; u < U; ++u) {
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (lane + 32 * u < mine) v[u] = load(lane + 32 * u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) m2 = q4_max2(m2, v[u]);
+    for (int j = lane + 32 * U; j < mine; j += 32) m2 = q4_max2(m2, load(j));  // (very long rows: loaded again below)
+  }
   uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-  if constexpr (WPR > 1) {
+  if (wpr > 1) {
     if (lane == 0) wmax[warp] = m;
     __syncthreads();
-    m = max(wmax[r * WPR], wmax[r * WPR + 1]);
+    m = wmax[lane < wpr ? r * wpr + lane : r * wpr];
+    m = __reduce_max_sync(0xffffffffu, m);
   }
-  // 2^110 over the power of two at or below it (1 for a row of zeros, and for
-  // one that holds an infinity or NaN: its sums are not finite anyway)
-  const int ex = (int)(m >> 7), sh = m == 0 || ex == 255 ? 0 : 237 - ex;
-  const float f1 = __int_as_float((127 + sh / 2) << 23), f2 = __int_as_float((127 + (sh - sh / 2)) << 23);
+  if (!live) return;
+  // 2^60 over the power of two at or below it (1 for a row of zeros, and for
+  // one that holds an infinity or NaN: its sums are not finite anyway), a
+  // sixteenth of it in the upper halves, the odd inputs; in two steps where
+  // that is above 2^127
+  const int ex = (int)(m >> 7), sh = m == 0 || ex == 255 ? 0 : 187 - ex, s1 = sh > 127 ? sh - 127 : 0, s2 = sh - s1;
+  const uint32_t f1 = (uint32_t)(127 + s1) * 0x00800080u, f2 = (uint32_t)(127 + s2) << 7 | (uint32_t)(123 + s2) << 23;
   if (lane == 0 && part == 0) {
     const int un = 133 - sh;
-    fac[4 * r] = __int_as_float((127 + un / 2) << 23);
-    fac[4 * r + 1] = __int_as_float((127 + (un - un / 2)) << 23);
+    fac[r] = make_float2(__int_as_float((127 + un / 2) << 23), __int_as_float((127 + (un - un / 2)) << 23));
   }
+  auto store = [&](int j, uint4 x) {
+    const int i = part + wpr * j;
+    if (s1) x = make_uint4(q4_mul2(x.x, f1), q4_mul2(x.y, f1), q4_mul2(x.z, f1), q4_mul2(x.w, f1));
+    x = make_uint4(q4_mul2(x.x, f2), q4_mul2(x.y, f2), q4_mul2(x.z, f2), q4_mul2(x.w, f2));
+    // in the order in which the nibbles of a word unpack (0 4 1 5 2 6 3 7);
+    // unit c of lane t in its group goes to place 4 c + t: a quad's reads are consecutive
+    const int in_g = i % (4 * W), at = i - in_g + 4 * (in_g % W) + in_g / W;
+    *reinterpret_cast<uint4*>(xs + (size_t)r * xp + 8 * at) =
+        make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                   __byte_perm(x.y, x.w, 0x7632));
+  };
 #pragma unroll
-  for (int u = 0; u < Q4_UNITS; ++u) {
-    const int i0 = 32 * (u * WPR + part), i = i0 + lane;
-    if (i0 < n8) {  // (the same for the whole warp)
-      const float x[8] = {bf16lo(v[u].x), bf16hi(v[u].x), bf16lo(v[u].y), bf16hi(v[u].y),
-                          bf16lo(v[u].z), bf16hi(v[u].z), bf16lo(v[u].w), bf16hi(v[u].w)};
-      float y[8], s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = x[e] * f1 * f2;
-        s += y[e];
-        if (e & 1) y[e] *= 0.0625f;
-      }
-#pragma unroll
-      for (int o = 1; o < G / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (i < n8) {
-        // in the order in which the nibbles of a word unpack
-        // (unit c of lane t in its group goes to place 4 c + t: a quad's reads are consecutive)
-        constexpr int W = G / 32;
-        const int in_g = i % (4 * W), at = i - in_g + 4 * (in_g % W) + in_g / W;
-        *reinterpret_cast<uint4*>(xs + (size_t)r * xp + 8 * at) =
-            make_uint4(pack_bf16x2(y[0], y[4]), pack_bf16x2(y[1], y[5]), pack_bf16x2(y[2], y[6]), pack_bf16x2(y[3], y[7]));
-        if (i % (G / 8) == 0) xg[i / (G / 8) * NR + r] = s * -0x1p-130f;
-      }
-    }
-  }
+  for (int u = 0; u < U; ++u)
+    if (lane + 32 * u < mine) store(lane + 32 * u, v[u]);
+  for (int j = lane + 32 * U; j < mine; j += 32) store(j, load(j));
 }
 
 // The epilogue's operands of one lane, loaded ahead of the products: the
@@ -524,7 +506,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
   extern __shared__ __align__(128) uint8_t q4_smem_buf[];
   __shared__ uint32_t wmax[Q4_WARPS];
   constexpr int NR = 8 * NT;            // rows of x held
-  constexpr int SLOT = q4_slot(G), RP = q4_rowpitch(G);
+  constexpr int SLOT = q4_slot(G), RP = Q4_RP;
   constexpr int GS = Q4_STAGE / G;      // groups of a stage
   constexpr int W = G / 32;             // words a lane has of a group
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -532,11 +514,11 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
   const int bx = blockIdx.x / a.split, gx = gridDim.x / a.split;
   const int k0 = rank * a.kr, kn = max(0, min(a.kr, a.K - k0));
   const int xp = q4_xpitch(a.kr);
-  const Q4Smem sm = q4_smem(NR, a.kr, G, a.split);
+  const Q4Smem sm = q4_smem(NR, a.rows, a.kr, G, a.part);
   bf16* xs = reinterpret_cast<bf16*>(q4_smem_buf);
   float* xg = reinterpret_cast<float*>(q4_smem_buf + sm.xg);
-  float* fac = reinterpret_cast<float*>(q4_smem_buf + sm.fac);
-  float4* red = reinterpret_cast<float4*>(q4_smem_buf + sm.red);    // [2][warps][NT][32]
+  float2* fac = reinterpret_cast<float2*>(q4_smem_buf + sm.fac);
+  float4* red = reinterpret_cast<float4*>(q4_smem_buf + sm.red);    // [warps][NT][32]
   float4* part = reinterpret_cast<float4*>(q4_smem_buf + sm.part);  // (split) [tiles][NT][32]
   const uint32_t ring = smem_u32(q4_smem_buf) + sm.ring + warp * a.ring * SLOT;
   const uint32_t ring_end = ring + a.ring * SLOT;
@@ -547,19 +529,23 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
   const int tstep = gx * gpb;
 
   // the producer side of this warp's ring: the next stage's sources (16 bytes
-  // of two rows of nibbles a lane, 16 bytes of scales), its tile and place
+  // of four rows of nibbles a lane, 16 bytes of scales), its tile and place
   const int nfull = kn / Q4_STAGE;
   int pt = si < nst ? grp * gx + bx : ntiles, ps = si;
   uint32_t pslot = ring;
-  const uint32_t dw = g * RP + 16 * t, dsc = Q4_COLS * RP + lane * 16;
-  const uint8_t *w0 = nullptr, *w1 = nullptr;
+  const int prow = lane >> 3, pc = lane & 7;
+  uint32_t dw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw[i] = (prow + 4 * i) * RP + 16 * q4_piece<G>(prow + 4 * i, pc);
+  const uint32_t dsc = Q4_COLS * RP + lane * 16;
+  const uint8_t* w[4] = {nullptr, nullptr, nullptr, nullptr};
   const bf16* scp = nullptr;
   bool sc_live = false;
   auto tile_sources = [&]() {
     const int n0 = pt * Q4_COLS, kk = k0 + ps * Q4_STAGE;
-    // columns past N read the last one and are dropped
-    w0 = a.W + ((size_t)min(n0 + g, a.N - 1) * a.K + kk) / 2 + 16 * t;
-    w1 = a.W + ((size_t)min(n0 + g + 8, a.N - 1) * a.K + kk) / 2 + 16 * t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // columns past N read the last one and are dropped
+      w[i] = a.W + ((size_t)min(n0 + prow + 4 * i, a.N - 1) * a.K + kk) / 2 + 16 * pc;
     // 16 columns of scales a group, 8 a copy (the pitch is a multiple of 8)
     const int c = n0 + 8 * (lane & 1);
     sc_live = lane < 2 * GS && c < a.pitch;
@@ -567,24 +553,24 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
   };
   if (pt < ntiles) tile_sources();
   const size_t sc_step = (size_t)ks * GS * a.pitch;
-  const int w_step = ks * (Q4_STAGE / 2);
+  const int w_step = ks * Q4_RP;
   auto issue = [&]() {
     if (pt < ntiles) {
       if (ps < nfull) {
-        cp_async16(pslot + dw, w0);
-        cp_async16(pslot + dw + 8 * RP, w1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async16(pslot + dw[i], w[i]);
         if (sc_live) cp_async16(pslot + dsc, scp);
       } else {
         const int left = kn - nfull * Q4_STAGE;  // (a multiple of 32 and of G)
-        if (t < left / 32) {
-          cp_async16(pslot + dw, w0);
-          cp_async16(pslot + dw + 8 * RP, w1);
+        if (pc < left / 32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cp_async16(pslot + dw[i], w[i]);
         }
         if (sc_live && (lane >> 1) * G < left) cp_async16(pslot + dsc, scp);
       }
       ps += ks;
-      w0 += w_step;
-      w1 += w_step;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] += w_step;
       scp += sc_step;
       if (ps >= nst) {
         ps = si;
@@ -603,19 +589,41 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
   if (!a.w_early) pdl_wait();
   for (int i = 0; i < a.ring - 1; ++i) issue();
   if (a.w_early) pdl_wait();
-  q4_stage_x<NR, G>(a, xs, xp, xg, fac, wmax, k0, kn, warp, lane);
+  q4_stage_x<G>(a, xs, xp, fac, wmax, k0, kn, warp, lane);
+  __syncthreads();
+  // this lane's rows of x (those past the last are not staged: the last one again, dropped)
+  uint32_t xrow[NT];
+#pragma unroll
+  for (int m = 0; m < NT; ++m) xrow[m] = smem_u32(xs) + (uint32_t)(min(g + 8 * m, a.rows - 1) * xp * 2 + 16 * t);
+  // -8 times the group sums: mma with every weight -8 (bits 0x8008, in the
+  // upper halves of bytes 0x8080)
+  for (int j = warp; j < kn / G; j += Q4_WARPS) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < W; ++c) {
+        const uint4 xv = lds128(xrow[m] + 64 * (W * j + c));
+        q4_mma(d, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, xv.x, xv.y);
+        q4_mma(d, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, xv.z, xv.w);
+      }
+      if (g == 0) *reinterpret_cast<float2*>(xg + j * NR + 8 * m + 2 * t) = make_float2(d[0], d[1]);
+    }
+  }
   __syncthreads();
 
-  const uint32_t xb = smem_u32(xs) + (uint32_t)(g * xp * 2 + 16 * t);
   const uint32_t xgb = smem_u32(xg) + (uint32_t)(2 * t * 4);
-  const uint32_t xm = (uint32_t)(8 * xp * 2);
+  const uint32_t sw = 16 * q4_piece<G>(g, 0);
   uint32_t cslot = ring;
   float acc[NT][4];
   // the products of groups [0, ng) of the stage in cslot, stage s of the k range
   auto stage = [&](int s, int ng) {
-    const uint32_t w = cslot + g * RP + 4 * W * t;
+    const uint32_t w = cslot + g * RP;
     const uint32_t sc = cslot + Q4_COLS * RP + 2 * g;
-    const uint32_t xk = xb + s * Q4_STAGE * 2, xgk = xgb + s * GS * NR * 4;
+    const uint32_t xgk = xgb + s * GS * NR * 4;
+    uint32_t xk[NT];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) xk[m] = xrow[m] + s * Q4_STAGE * 2;
 #pragma unroll
     for (int j = 0; j < GS; ++j) {
       if (j < ng) {
@@ -629,15 +637,17 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
           c1[m][0] = c1[m][1] = c1[m][2] = c1[m][3] = 0.f;
         }
         uint32_t wa[W], wb[W];
-        lds_words<W>(w + 16 * W * j, wa);
-        lds_words<W>(w + 8 * RP + 16 * W * j, wb);
+        // (the pieces of rows g and g + 8 are exchanged alike)
+        const uint32_t at = ((16 * W * j) ^ sw) + 4 * W * t;
+        lds_words<W>(w + at, wa);
+        lds_words<W>(w + 8 * RP + at, wb);
 #pragma unroll
         for (int c = 0; c < W; ++c) {
           constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
           const uint32_t va = wa[c] >> 8, vb = wb[c] >> 8;
 #pragma unroll
           for (int m = 0; m < NT; ++m) {
-            const uint4 xv = lds128(xk + m * xm + 64 * (W * j + c));
+            const uint4 xv = lds128(xk[m] + 64 * (W * j + c));
             q4_mma(c0[m], wa[c] & LO, wb[c] & LO, wa[c] & HI, wb[c] & HI, xv.x, xv.y);
             q4_mma(W > 1 ? c1[m] : c0[m], va & LO, vb & LO, va & HI, vb & HI, xv.z, xv.w);
           }
@@ -651,8 +661,8 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
       }
     }
   };
-  int par = 0, it = 0;
-  const int ptg = Q4_PART_TILES / gpb;  // (split) tile passes between exchanges
+  int it = 0;
+  const int ptg = max(1, a.part / gpb);  // (split) tile passes between exchanges
   for (int base = bx; base < ntiles; base += tstep) {
     const int tile = base + grp * gx;
     const bool joins = si == it % ks;  // the warps of a tile take turns at its epilogue
@@ -672,15 +682,13 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
         cslot = cslot + SLOT == ring_end ? ring : cslot + SLOT;
       }
     }
-    // the tile's warps meet: two buffers in turn, a buffer is written again
-    // only after the next barrier, which the warp that read it has then reached
-    float4* rb = red + par * (Q4_WARPS * NT * 32);
-    par ^= 1;
+    // the tile's warps meet: once all are here the sums of the last tile have been read
     float4 tot[NT];
     if (ks > 1) {
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ks * 32) : "memory");
 #pragma unroll
       for (int m = 0; m < NT; ++m)
-        rb[(warp * NT + m) * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+        red[(warp * NT + m) * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
       asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(ks * 32) : "memory");
     }
     if (joins) {
@@ -690,7 +698,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
           tot[m] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int x = 0; x < ks; ++x) {
-            const float4 q = rb[((grp * ks + x) * NT + m) * 32 + lane];
+            const float4 q = red[((grp * ks + x) * NT + m) * 32 + lane];
             tot[m].x += q.x;
             tot[m].y += q.y;
             tot[m].z += q.z;
@@ -700,8 +708,7 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
           tot[m] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
         }
         // out of the row's scaling and the nibbles' 2^-133
-        const float2 fa = *reinterpret_cast<const float2*>(fac + 4 * (8 * m + 2 * t));
-        const float2 fb = *reinterpret_cast<const float2*>(fac + 4 * (8 * m + 2 * t + 1));
+        const float2 fa = fac[8 * m + 2 * t], fb = fac[8 * m + 2 * t + 1];
         tot[m].x = tot[m].x * fa.x * fa.y;
         tot[m].y = tot[m].y * fb.x * fb.y;
         tot[m].z = tot[m].z * fa.x * fa.y;
@@ -747,10 +754,137 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// The same products for few tiles, where the time is that of one round trip to
+// memory and not of the stream: staging x, which pays off over many tiles of
+// a block, would cost more than it saves.  A block of 16 warps takes one
+// tile of 16 columns, its warps every 16th unit of max(G, 64) inputs; nibbles
+// and x come straight from memory as fragments, a unit ahead.  Here a nibble
+// is converted: bf16 bits 0x4300 | nibble are 128 + nibble, and one packed
+// subtraction of 136 leaves two q exactly.
+constexpr int QD_WARPS = 16;
+DEVI uint32_t q4_pair(uint32_t w, int i) { return q4_sub136(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u); }
+
+template <int NT, int G>
+__global__ void __launch_bounds__(QD_WARPS * 32) q4_direct_kernel(const __grid_constant__ Q4Args a) {
+  constexpr int W = G / 32;                     // words a lane has of a group
+  constexpr int UG = G < 64 ? 2 : 1;            // groups of a unit
+  constexpr int UK = UG * G;                    // inputs of a unit
+  __shared__ float4 red[QD_WARPS][NT][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * Q4_COLS, nun = (a.K + UK - 1) / UK;
+  // columns and rows past the last read the last one and are dropped
+  const uint8_t* wa = a.W + (size_t)min(n0 + g, a.N - 1) * a.K / 2 + 4 * W * t;
+  const uint8_t* wb = a.W + (size_t)min(n0 + g + 8, a.N - 1) * a.K / 2 + 4 * W * t;
+  const bf16* x[NT];
+#pragma unroll
+  for (int m = 0; m < NT; ++m)
+    x[m] = reinterpret_cast<const bf16*>(a.in) + (size_t)min(g + 8 * m, a.rows - 1) * a.ldi + 8 * W * t;
+  const bf16* sa = a.sc + min(n0 + g, a.N - 1);
+  const bf16* sb = a.sc + min(n0 + g + 8, a.N - 1);
+  struct Unit {
+    uint32_t wa[UG][W], wb[UG][W];
+    uint4 x[NT][UG][W];
+    float s0[UG], s1[UG];
+  };
+  pdl_trigger();
+  if (!a.w_early) pdl_wait();
+  auto load_w = [&](Unit& u, int i) {
+#pragma unroll
+    for (int j = 0; j < UG; ++j) {
+      const int k = i * UK + j * G;
+      const bool in = i < nun && k < a.K;
+#pragma unroll
+      for (int c = 0; c < W; ++c) u.wa[j][c] = u.wb[j][c] = 0x88888888u;
+      u.s0[j] = u.s1[j] = 0.f;
+      if (in) {
+        if constexpr (W == 4) {
+          const uint4 p = *reinterpret_cast<const uint4*>(wa + k / 2), q = *reinterpret_cast<const uint4*>(wb + k / 2);
+          u.wa[j][0] = p.x; u.wa[j][1] = p.y; u.wa[j][2] = p.z; u.wa[j][3] = p.w;
+          u.wb[j][0] = q.x; u.wb[j][1] = q.y; u.wb[j][2] = q.z; u.wb[j][3] = q.w;
+        } else if constexpr (W == 2) {
+          const uint2 p = *reinterpret_cast<const uint2*>(wa + k / 2), q = *reinterpret_cast<const uint2*>(wb + k / 2);
+          u.wa[j][0] = p.x; u.wa[j][1] = p.y;
+          u.wb[j][0] = q.x; u.wb[j][1] = q.y;
+        } else {
+          u.wa[j][0] = *reinterpret_cast<const uint32_t*>(wa + k / 2);
+          u.wb[j][0] = *reinterpret_cast<const uint32_t*>(wb + k / 2);
+        }
+        u.s0[j] = to_f(sa[(size_t)(k / G) * a.pitch]);
+        u.s1[j] = to_f(sb[(size_t)(k / G) * a.pitch]);
+      }
+    }
+  };
+  auto load_x = [&](Unit& u, int i) {
+#pragma unroll
+    for (int j = 0; j < UG; ++j) {
+      const int k = i * UK + j * G;
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int c = 0; c < W; ++c)
+          u.x[m][j][c] = i < nun && k < a.K ? *reinterpret_cast<const uint4*>(x[m] + k + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  Unit cur, next;
+  load_w(cur, warp);
+  if (a.w_early) pdl_wait();
+  load_x(cur, warp);
+  Q4Pre<NT> pre;
+  if (warp == 0) q4_preload<NT>(a, pre, n0, g, t);
+  float acc[NT][4];
+#pragma unroll
+  for (int m = 0; m < NT; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+  for (int i = warp; i < nun; i += QD_WARPS) {
+    load_w(next, i + QD_WARPS);
+    load_x(next, i + QD_WARPS);
+#pragma unroll
+    for (int j = 0; j < UG; ++j) {
+      float c0[NT][4];
+#pragma unroll
+      for (int m = 0; m < NT; ++m) c0[m][0] = c0[m][1] = c0[m][2] = c0[m][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < W; ++c) {
+        const uint32_t p = cur.wa[j][c], q = cur.wb[j][c];
+        const uint32_t p0 = q4_pair(p, 0), q0 = q4_pair(q, 0), p1 = q4_pair(p, 1), q1 = q4_pair(q, 1);
+        const uint32_t p2 = q4_pair(p, 2), q2 = q4_pair(q, 2), p3 = q4_pair(p, 3), q3 = q4_pair(q, 3);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          const uint4 v = cur.x[m][j][c];  // into the nibbles' order: 0 4, 1 5, 2 6, 3 7
+          q4_mma(c0[m], p0, q0, p1, q1, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
+          q4_mma(c0[m], p2, q2, p3, q3, __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(e < 2 ? cur.s0[j] : cur.s1[j], c0[m][e], acc[m][e]);
+    }
+    cur = next;
+  }
+#pragma unroll
+  for (int m = 0; m < NT; ++m) red[warp][m][lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      float4 tot = red[0][m][lane];
+#pragma unroll
+      for (int y = 1; y < QD_WARPS; ++y) {
+        const float4 v = red[y][m][lane];
+        tot.x += v.x;
+        tot.y += v.y;
+        tot.z += v.z;
+        tot.w += v.w;
+      }
+      q4_epilogue<NT>(a, tot, pre, m, n0, g, t);
+    }
+  }
+}
+
 // How a product is spread over the machine: the k range of a block (the
 // cluster split), the warps that share a tile and the depth of the rings.
 struct Q4Plan {
-  int split, kr, ks, ring, grid;
+  int split, kr, ks, ring, part, grid;
   size_t smem;
 };
 bool q4_plan(int rows, int N, int K, int group, bool ln, Q4Plan* p) {
@@ -759,13 +893,12 @@ bool q4_plan(int rows, int N, int K, int group, bool ln, Q4Plan* p) {
   const int nst = (K + Q4_STAGE - 1) / Q4_STAGE, ntiles = (N + Q4_COLS - 1) / Q4_COLS;
   for (p->split = 1; p->split <= Q4_MAX_SPLIT; p->split *= 2) {
     p->kr = p->split == 1 ? K : (nst + p->split - 1) / p->split * Q4_STAGE;
-    if (NR * p->kr > Q4_WARPS * 32 * 8 * Q4_UNITS) continue;  // more than the lanes hold while staging
-    const size_t fixed = q4_smem(NR, p->kr, group, p->split).ring + 256;  // (256: the kernel's static words)
+    p->part = p->split > 1 ? Q4_PART_TILES : 0;
+    if (p->split > 1 && q4_smem(NR, rows, p->kr, group, p->part).ring + 256 + 2 * Q4_WARPS * slot > Q4_SMEM) p->part = 1;
+    const size_t fixed = q4_smem(NR, rows, p->kr, group, p->part).ring + 256;  // (256: the kernel's static words)
     if (fixed + (size_t)Q4_WARPS * 2 * slot > Q4_SMEM) continue;
     const int ring = (int)((Q4_SMEM - fixed) / ((size_t)Q4_WARPS * slot));
-    // a shallow ring starves the stream: split further while that is possible
-    if (ring < 4 && p->split < Q4_MAX_SPLIT && !ln) continue;
-    p->ring = ring >= 6 ? 6 : (ring >= 4 ? 4 : 2);
+    p->ring = ring < 4 ? ring : 4;
     p->smem = fixed - 256 + (size_t)Q4_WARPS * p->ring * slot;
     break;
   }
@@ -775,9 +908,9 @@ bool q4_plan(int rows, int N, int K, int group, bool ln, Q4Plan* p) {
   const int st = (p->kr + Q4_STAGE - 1) / Q4_STAGE;
   for (int ks = 1; ks <= Q4_WARPS; ks *= 2) {
     const int gpb = Q4_WARPS / ks;
-    if (p->split > 1 && gpb > Q4_PART_TILES) continue;
+    if (p->split > 1 && gpb > p->part) continue;
     const int per_block = (ntiles + slots - 1) / slots, passes = (per_block + gpb - 1) / gpb;
-    const long cost = (long)passes * ((st + ks - 1) / ks + 2);
+    const long cost = (long)passes * (2 * ((st + ks - 1) / ks) + 2);
     if (best < 0 || cost < best) {
       best = cost;
       p->ks = ks;
@@ -811,10 +944,21 @@ int q4_launch(Q4Args& a, const Q4Plan& p, cudaStream_t st) {
   return GPT2_OK;
 }
 
-int q4_run(Q4Args& a, int group, cudaStream_t st) {
-  Q4Plan p;
-  if (!q4_plan(a.rows, a.N, a.K, group, a.ln != 0, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
-  a.ks = p.ks; a.split = p.split; a.kr = p.kr; a.ring = p.ring;
+template <int NT>
+int q4_direct(const Q4Args& a, int group, cudaStream_t st) {
+  const unsigned grid = (unsigned)((a.N + Q4_COLS - 1) / Q4_COLS);
+  if (group == 32) CUDA_TRY(launch_k(q4_direct_kernel<NT, 32>, grid, QD_WARPS * 32, 0, st, a));
+  else if (group == 64) CUDA_TRY(launch_k(q4_direct_kernel<NT, 64>, grid, QD_WARPS * 32, 0, st, a));
+  else CUDA_TRY(launch_k(q4_direct_kernel<NT, 128>, grid, QD_WARPS * 32, 0, st, a));
+  LAUNCH_CHECK();
+  return GPT2_OK;
+}
+
+int q4_launch_rows(Q4Args& a, const Q4Plan& p, int group, cudaStream_t st) {
+  a.ks = p.ks; a.split = p.split; a.kr = p.kr; a.ring = p.ring; a.part = p.part;
+  int rows2 = 1;
+  while (rows2 < a.rows) rows2 *= 2;
+  a.wpr = Q4_WARPS / rows2;
   if (a.rows <= 8) {
     if (group == 32) return q4_launch<1, 32>(a, p, st);
     if (group == 64) return q4_launch<1, 64>(a, p, st);
@@ -823,6 +967,38 @@ int q4_run(Q4Args& a, int group, cudaStream_t st) {
   if (group == 32) return q4_launch<2, 32>(a, p, st);
   if (group == 64) return q4_launch<2, 64>(a, p, st);
   return q4_launch<2, 128>(a, p, st);
+}
+
+int q4_run(Q4Args& a, int group, cudaStream_t st) {
+  // Few weights: the direct kernel.  Measured on both sides, in us (direct,
+  // streamed): groups of 64 and 128, N K 7.7e6 (4800 x 1600, 1 row) 4.9, 5.8,
+  // 1e7 (1600 x 6400, 8 rows) 6.0, 10.2 and 1.2e7 (16000 x 768, 16 rows) 9.7, 8.0;
+  // groups of 32, whose lanes load 4 bytes at a time, 3.7e6 (2304 x 1600, 8
+  // rows) 4.0, 5.6 and 7.7e6 (4800 x 1600, 16 rows) 10.5, 8.2.
+  const double weights = (double)a.N * a.K;
+  if (!a.ln && !a.in_f32 && weights <= (group == 32 ? 6 << 20 : 10 << 20))
+    return a.rows <= 8 ? q4_direct<1>(a, group, st) : q4_direct<2>(a, group, st);
+  // Rows that do not fit shared memory together: in up to three groups, each a
+  // pass over the weights, else split over clusters (16 rows: 50304 x 6400 75 us
+  // in two passes, 185 us over clusters; 8 rows, 8192 x 28672 145 us in four).
+  Q4Plan p;
+  for (int groups = 1; groups <= (a.ln ? 1 : 3); ++groups) {
+    const int per = (a.rows + groups - 1) / groups;
+    if (!q4_plan(per, a.N, a.K, group, a.ln != 0, &p) || (p.split > 1 && !a.ln)) continue;
+    const int rows = a.rows;
+    for (int r0 = 0; r0 < rows; r0 += per) {
+      Q4Args b = a;
+      b.rows = rows - r0 < per ? rows - r0 : per;
+      b.in = reinterpret_cast<const uint8_t*>(a.in) + (size_t)r0 * a.ldi * (a.in_f32 || a.ln ? 4 : 2);
+      b.out = reinterpret_cast<uint8_t*>(a.out) + (size_t)r0 * a.ldo * (a.epi == Q4_BF16 || a.epi == Q4_GELU ? 2 : 4);
+      if (!q4_plan(b.rows, a.N, a.K, group, a.ln != 0, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
+      const int rc = q4_launch_rows(b, p, group, st);
+      if (rc != GPT2_OK) return rc;
+    }
+    return GPT2_OK;
+  }
+  if (!q4_plan(a.rows, a.N, a.K, group, a.ln != 0, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  return q4_launch_rows(a, p, group, st);
 }
 
 // (K: at most 65535 k blocks of a grid)
