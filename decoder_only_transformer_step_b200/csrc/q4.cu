@@ -759,13 +759,56 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
 // a block, would cost more than it saves.  A block of 16 warps takes one
 // tile of 16 columns, its warps every 16th unit of max(G, 64) inputs; nibbles
 // and x come straight from memory as fragments, a unit ahead.  Here a nibble
-// is converted: bf16 bits 0x4300 | nibble are 128 + nibble, and one packed
-// subtraction of 136 leaves two q exactly.
+// is converted: bf16 bits 0x3e00 | nibble are (128 + nibble) / 1024, and one
+// packed subtraction of 136 / 1024 leaves two q / 1024 exactly (a group's sum
+// of up to 128 products |q| <= 8 then stays in range whatever x is; the scale
+// takes the 1024 back).  fp32 or LayerNorm'd rows are first
+// brought into shared memory as bf16 (STAGED; one warp a row).
 constexpr int QD_WARPS = 16;
-DEVI uint32_t q4_pair(uint32_t w, int i) { return q4_sub136(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u); }
+constexpr int QD_STAGED_K = 2048;  // widest staged row
+constexpr int QD_PAD = 32;         // elements behind a staged row: an odd multiple of 64 bytes in all
+DEVI uint32_t q4_pair(uint32_t w, int i) {
+  const uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x3e003e00u, c = 0x3e083e08u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-template <int NT, int G>
+// Row r of the fp32 input, LayerNorm'd if a.ln, as bf16; a whole warp.
+DEVI void q4_stage_row(const Q4Args& a, bf16* dst, int r, int lane) {
+  const float* src = reinterpret_cast<const float*>(a.in) + (size_t)r * a.ldi;
+  const int n4 = a.K / 4;
+  float mu = 0.f, rs = 1.f;
+  if (a.ln) {
+    float s = 0.f, q = 0.f;
+#pragma unroll 8
+    for (int i = lane; i < n4; i += 32) {
+      const float4 f = *reinterpret_cast<const float4*>(src + 4 * i);
+      s += (f.x + f.y) + (f.z + f.w);
+    }
+    mu = warp_sum(s) / a.K;
+#pragma unroll 8
+    for (int i = lane; i < n4; i += 32) {
+      const float4 f = *reinterpret_cast<const float4*>(src + 4 * i);
+      const float t0 = f.x - mu, t1 = f.y - mu, t2 = f.z - mu, t3 = f.w - mu;
+      q += (t0 * t0 + t1 * t1) + (t2 * t2 + t3 * t3);
+    }
+    rs = rsqrtf(warp_sum(q) / a.K + 1e-5f);
+  }
+#pragma unroll 4
+  for (int i = lane; i < n4; i += 32) {
+    float4 f = *reinterpret_cast<const float4*>(src + 4 * i);
+    if (a.ln) {
+      const float4 gg = q4_ld4(a.ln_g + 4 * i), bb = q4_ld4(a.ln_b + 4 * i);
+      f = make_float4((f.x - mu) * rs * gg.x + bb.x, (f.y - mu) * rs * gg.y + bb.y, (f.z - mu) * rs * gg.z + bb.z,
+                      (f.w - mu) * rs * gg.w + bb.w);
+    }
+    *reinterpret_cast<uint2*>(dst + 4 * i) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+  }
+}
+
+template <int NT, int G, bool STAGED>
 __global__ void __launch_bounds__(QD_WARPS * 32) q4_direct_kernel(const __grid_constant__ Q4Args a) {
+  extern __shared__ __align__(16) uint8_t qd_smem[];  // (STAGED) the rows
   constexpr int W = G / 32;                     // words a lane has of a group
   constexpr int UG = G < 64 ? 2 : 1;            // groups of a unit
   constexpr int UK = UG * G;                    // inputs of a unit
@@ -775,10 +818,13 @@ __global__ void __launch_bounds__(QD_WARPS * 32) q4_direct_kernel(const __grid_c
   // columns and rows past the last read the last one and are dropped
   const uint8_t* wa = a.W + (size_t)min(n0 + g, a.N - 1) * a.K / 2 + 4 * W * t;
   const uint8_t* wb = a.W + (size_t)min(n0 + g + 8, a.N - 1) * a.K / 2 + 4 * W * t;
+  bf16* const xs = reinterpret_cast<bf16*>(qd_smem);
   const bf16* x[NT];
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
-    x[m] = reinterpret_cast<const bf16*>(a.in) + (size_t)min(g + 8 * m, a.rows - 1) * a.ldi + 8 * W * t;
+  for (int m = 0; m < NT; ++m) {
+    const size_t r = min(g + 8 * m, a.rows - 1);
+    x[m] = (STAGED ? xs + r * (a.K + QD_PAD) : reinterpret_cast<const bf16*>(a.in) + r * a.ldi) + 8 * W * t;
+  }
   const bf16* sa = a.sc + min(n0 + g, a.N - 1);
   const bf16* sb = a.sc + min(n0 + g + 8, a.N - 1);
   struct Unit {
@@ -809,8 +855,8 @@ __global__ void __launch_bounds__(QD_WARPS * 32) q4_direct_kernel(const __grid_c
           u.wa[j][0] = *reinterpret_cast<const uint32_t*>(wa + k / 2);
           u.wb[j][0] = *reinterpret_cast<const uint32_t*>(wb + k / 2);
         }
-        u.s0[j] = to_f(sa[(size_t)(k / G) * a.pitch]);
-        u.s1[j] = to_f(sb[(size_t)(k / G) * a.pitch]);
+        u.s0[j] = 1024.f * to_f(sa[(size_t)(k / G) * a.pitch]);
+        u.s1[j] = 1024.f * to_f(sb[(size_t)(k / G) * a.pitch]);
       }
     }
   };
@@ -828,6 +874,10 @@ __global__ void __launch_bounds__(QD_WARPS * 32) q4_direct_kernel(const __grid_c
   Unit cur, next;
   load_w(cur, warp);
   if (a.w_early) pdl_wait();
+  if constexpr (STAGED) {
+    for (int r = warp; r < a.rows; r += QD_WARPS) q4_stage_row(a, xs + (size_t)r * (a.K + QD_PAD), r, lane);
+    __syncthreads();
+  }
   load_x(cur, warp);
   Q4Pre<NT> pre;
   if (warp == 0) q4_preload<NT>(a, pre, n0, g, t);
@@ -944,14 +994,22 @@ int q4_launch(Q4Args& a, const Q4Plan& p, cudaStream_t st) {
   return GPT2_OK;
 }
 
-template <int NT>
-int q4_direct(const Q4Args& a, int group, cudaStream_t st) {
-  const unsigned grid = (unsigned)((a.N + Q4_COLS - 1) / Q4_COLS);
-  if (group == 32) CUDA_TRY(launch_k(q4_direct_kernel<NT, 32>, grid, QD_WARPS * 32, 0, st, a));
-  else if (group == 64) CUDA_TRY(launch_k(q4_direct_kernel<NT, 64>, grid, QD_WARPS * 32, 0, st, a));
-  else CUDA_TRY(launch_k(q4_direct_kernel<NT, 128>, grid, QD_WARPS * 32, 0, st, a));
+template <int NT, int G, bool STAGED>
+int q4_direct_launch(const Q4Args& a, cudaStream_t st) {
+  const size_t smem = STAGED ? (size_t)a.rows * (a.K + QD_PAD) * sizeof(bf16) : 0;
+  CUDA_TRY(once_per_device((const void*)q4_direct_kernel<NT, G, STAGED>, [](int) {
+    return cudaFuncSetAttribute(q4_direct_kernel<NT, G, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                16 * (QD_STAGED_K + QD_PAD) * (int)sizeof(bf16));
+  }));
+  CUDA_TRY(launch_k(q4_direct_kernel<NT, G, STAGED>, (unsigned)((a.N + Q4_COLS - 1) / Q4_COLS), QD_WARPS * 32, smem, st, a));
   LAUNCH_CHECK();
   return GPT2_OK;
+}
+template <int NT, bool STAGED>
+int q4_direct(const Q4Args& a, int group, cudaStream_t st) {
+  if (group == 32) return q4_direct_launch<NT, 32, STAGED>(a, st);
+  if (group == 64) return q4_direct_launch<NT, 64, STAGED>(a, st);
+  return q4_direct_launch<NT, 128, STAGED>(a, st);
 }
 
 int q4_launch_rows(Q4Args& a, const Q4Plan& p, int group, cudaStream_t st) {
@@ -976,8 +1034,12 @@ int q4_run(Q4Args& a, int group, cudaStream_t st) {
   // groups of 32, whose lanes load 4 bytes at a time, 3.7e6 (2304 x 1600, 8
   // rows) 4.0, 5.6 and 7.7e6 (4800 x 1600, 16 rows) 10.5, 8.2.
   const double weights = (double)a.N * a.K;
-  if (!a.ln && !a.in_f32 && weights <= (group == 32 ? 6 << 20 : 10 << 20))
-    return a.rows <= 8 ? q4_direct<1>(a, group, st) : q4_direct<2>(a, group, st);
+  if (weights <= (group == 32 ? 6 << 20 : 10 << 20)) {
+    if (!a.ln && !a.in_f32) return a.rows <= 8 ? q4_direct<1, false>(a, group, st) : q4_direct<2, false>(a, group, st);
+    // (every block stages all rows: at 2304 x 768 a decode step of 12 layers takes 354 us, streamed 423; at
+    // 4800 x 1600 one of 48 layers 2550 us, streamed 2000)
+    if (a.K <= QD_STAGED_K && weights <= 3 << 20) return a.rows <= 8 ? q4_direct<1, true>(a, group, st) : q4_direct<2, true>(a, group, st);
+  }
   // Rows that do not fit shared memory together: in up to three groups, each a
   // pass over the weights, else split over clusters (16 rows: 50304 x 6400 75 us
   // in two passes, 185 us over clusters; 8 rows, 8192 x 28672 145 us in four).

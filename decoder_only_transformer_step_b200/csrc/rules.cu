@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
       mbar_init(smem_u32(&arrived), 1);
       mbar_fence_init();
     }
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   if constexpr (COUNTED) {
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
     }
   }
   if (!a.next) return;
+  __syncwarp();
   if (meets) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {

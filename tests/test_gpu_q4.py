@@ -196,3 +196,33 @@ def test_bf16_weights_at_and_around_halves(scale):
     q, s = reference_quantise(t.float().cpu().numpy(), group)
     np.testing.assert_array_equal(scales.float().cpu().numpy(), s.T)
     np.testing.assert_array_equal(unpack(packed), q)
+
+
+@pytest.mark.parametrize("N,K,group", [(100, 512, 64), (3000, 1536, 32), (2100, 5376, 128)])
+@pytest.mark.parametrize("rows", [4, 11])
+def test_rows_of_any_magnitude_and_rows_that_are_not_finite(N, K, group, rows):
+    # each row has a scale of its own, from the type's largest values to its subnormal ones; inside a row the
+    # magnitudes span 2^40.  The tolerance is that of gemv_case, for the order of sums only: nothing else rounds.
+    rng = np.random.default_rng(N)
+    nib = rng.integers(1, 16, size=(N, K)).astype(np.uint8)
+    packed = torch.from_numpy(nib[:, 0::2] | (nib[:, 1::2] << 4)).cuda()
+    scales = torch.zeros(K // group, pitch(N), device="cuda").bfloat16()
+    scales[:, :N] = torch.from_numpy(2.0 ** rng.integers(-12, -8, (K // group, N))).cuda()
+    x = torch.from_numpy(rng.standard_normal((rows, K)) * 2.0 ** rng.integers(-40, 1, (rows, K)))
+    x = (x * torch.tensor([[3e37], [1e-37], [3e-39], [1.0]][:4] + [[2e5]] * (rows - 4))).bfloat16().cuda()
+    y = torch.empty(rows, N, device="cuda")
+    gp.gpt2_op_gemv_q4(x, K, packed, scales, None, y, 1, N, rows, N, K, group)
+    W = torch.from_numpy(nib.astype(np.float64) - 8).cuda() * scales[:, :N].double().t().repeat_interleave(group, 1)
+    want, mag = x.double() @ W.t(), x.double().abs() @ W.abs().t()
+    depth = (group // 32) * 17 + K / group + 16 + 8 + 3
+    # (results below the smallest normal number are held in steps of 2^-149; x's two powers of two round once each)
+    tol = depth * 2.0**-23 * mag + 2.0**-24 * want.abs() + 2.0**-148
+    # -8 sum x starts a group's sum: its terms are in mag up to a factor 8 / |q| <= 8
+    tol = tol + depth * 2.0**-23 * 8 * (x.double().abs() @ (W.abs() / (torch.from_numpy(nib.astype(np.float64) - 8).abs().cuda() + (torch.from_numpy(nib).cuda() == 8))).t())
+    assert bool(((y.double() - want).abs() <= tol).all()), float(((y.double() - want).abs() / tol).max())
+    x[1, 5], x[2, 7] = float("inf"), float("nan")
+    z = torch.empty_like(y)
+    gp.gpt2_op_gemv_q4(x, K, packed, scales, None, z, 1, N, rows, N, K, group)
+    assert not bool(torch.isfinite(z[1:3]).any())
+    keep = [r for r in range(rows) if r not in (1, 2)]
+    assert torch.equal(z[keep], y[keep])

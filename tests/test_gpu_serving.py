@@ -91,16 +91,20 @@ def test_rows_behind_a_prefix_match_the_oracle_on_whole_sequences(oc, mode, P):
     assert torch.equal(before[:planes], pre.buf[:planes])   # the prefix is only read
 
 
-@pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("batch", [1, 8, 13])
-def test_decode_with_4_bit_weights_matches_the_oracle_on_their_values(group, batch):
-    oc = HD64
+# wide enough that the products stream their weights (the narrow ones above read them directly)
+WIDE = Config(n_layer=1, d_model=1280, n_head=20, n_ctx=64, vocab=2560)
+
+
+@pytest.mark.parametrize("oc,group,batch", [(HD64, g, b) for g in (32, 64, 128) for b in (1, 8, 13)] +
+                         [(WIDE, g, b) for g in (32, 128) for b in (3, 16)],
+                         ids=lambda v: "wide" if v is WIDE else "narrow" if v is HD64 else str(v))
+def test_decode_with_4_bit_weights_matches_the_oracle_on_their_values(oc, group, batch):
     model, _ = make_model(oc, 0, batch=16)
     q4 = gp.Q4Weights(model, group)
     p64, head = rounded(model, oc, group)
     cache = gp.KVCache(model, batch, 16, q4=q4)
     ref = kv_cache_empty(oc, batch, 16)
-    for step in range(6):
+    for step in range(6 if oc is HD64 else 3):
         tok = inputs.uniform_tokens(batch, 1, oc.vocab - 12, seed=300 + step)[0][:, 0]
         pos = np.full(batch, step, np.int32)
         z = cache.step(i32(tok), i32(pos)).cpu().numpy().astype(np.float64)
