@@ -25,8 +25,14 @@ constexpr int PA_MIN_PART = PA_WARPS * 32;
 constexpr int PA_DIRECT_KEYS = 1024;       // a block takes all keys of its rows up to so many keys a row
 constexpr double PA_DIRECT_BYTES = 8e6;    //   and so many bytes that the whole batch reads that way
 constexpr int PT_BLOCKS = 148;   // blocks of the tcgen05 kernel: one an SM
-constexpr int PT_MIN_ROWS = 16;  // it is taken above so many query rows of a key/value head
-constexpr int PT_MIN_KEYS = 1024;
+// The tcgen05 kernel is taken from so many query rows of a key/value head on,
+// where their products with the prefix are so many (rows x keys x hd).
+// Measured on both sides, in us (tcgen05, mma.sync): 48 rows, 16384 keys of 128,
+// 8 heads (1.0e8) 27.5, 28.6; 128 rows, 16384 keys of 64, 12 heads (1.3e8) 39, 47;
+// 128 rows, 3500 keys of 128 (5.7e7) 26.3, 26.7; 64 rows, 16384 keys of 64 (6.7e7)
+// 31, 27; 32 rows, 16384 keys of 128 26.4, 24.0.
+constexpr int PT_MIN_ROWS = 48;
+constexpr double PT_MIN_WORK = 9e7;
 
 struct PrefixArgs {
   const void* q;  // [B, ldq], bf16 or fp32 (rounded to bf16 on load)
@@ -785,7 +791,7 @@ bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan*
   };
   p->direct = (long)P + max_len <= PA_DIRECT_KEYS &&
               (double)own_blocks * ((double)P + max_len) * hd * 4 <= PA_DIRECT_BYTES;
-  p->tc = !p->direct && hd >= 64 && M > PT_MIN_ROWS && P >= PT_MIN_KEYS;
+  p->tc = !p->direct && hd >= 64 && M >= PT_MIN_ROWS && (double)M * P * hd >= PT_MIN_WORK;
   if (p->tc) {
     const long max_rows = M <= 128 ? 128 : 256;
     p->mtp = (int)((M + max_rows - 1) / max_rows);

@@ -113,9 +113,27 @@ def test_many_rows_on_the_tensor_cores(hd, B, Hq, Hkv, P):
     check(s)
 
 
+@pytest.mark.parametrize("hd,B,Hq,Hkv,P", [(64, 48, 1, 1, 29400), (64, 65, 2, 1, 11007), (64, 128, 2, 2, 11001),
+                                           (64, 43, 3, 1, 10950), (64, 300, 1, 1, 4750), (64, 257, 2, 1, 3000),
+                                           (128, 96, 1, 1, 7424), (128, 129, 2, 2, 5500), (128, 40, 32, 8, 4500),
+                                           (128, 128, 1, 1, 5569), (128, 100, 8, 1, 1024), (128, 520, 1, 1, 1500)])
+def test_much_work_on_the_tensor_cores(hd, B, Hq, Hkv, P):
+    s = make(B, Hq, Hkv, hd, P, 20, [(b * 7) % 21 for b in range(B)], seed=P + B, cap=P + 5, ldq=Hq * hd + (B % 2) * 2,
+             ldo=Hq * hd + 4)
+    s["pk"][:, P:] = float("nan")
+    s["pv"][:, P:] = float("inf")
+    call(s)
+    check(s)
+
+
 def test_maxima_that_keep_growing():
     # keys ordered so that every block raises the maxima: the running sums are rescaled again and again
     s = make(40, 4, 1, 128, 3000, 0, [0] * 40, seed=8, q_std=3.0)
+    s["q"] = s["q"].abs()
+    s["pk"] = (s["pk"].abs() * torch.linspace(0.0, 1.5, 3000, device="cuda")[None, :, None]).bfloat16()
+    call(s)
+    check(s)
+    s = make(80, 4, 1, 128, 3000, 0, [0] * 80, seed=9, q_std=3.0)   # the same on the tensor cores
     s["q"] = s["q"].abs()
     s["pk"] = (s["pk"].abs() * torch.linspace(0.0, 1.5, 3000, device="cuda")[None, :, None]).bfloat16()
     call(s)
