@@ -440,13 +440,14 @@ def _torch():
 
 
 def _buf(where, name, t, dtype, dev, need):
-    """Address of a buffer on device `dev` of at least `need` elements (counted
-    up to a strided view's last one); None for None where none are needed."""
+    """Address of a buffer on device `dev` of at least `need` elements (of a
+    strided view: the memory from its first to its last one, which an expanded
+    tensor has less of than elements); None for None where none are needed."""
     if t is None:
         if need <= 0:
             return None
         raise Gpt2Error(-1, f"{where}: {name} is missing")
-    if t.dtype is dtype and t.get_device() == dev and (t.numel() >= need or _span(t) >= need):
+    if t.dtype is dtype and t.get_device() == dev and (t.numel() if t.is_contiguous() else _span(t)) >= need:
         return t.data_ptr()
     if t.dtype is not dtype:
         raise Gpt2Error(-1, f"{where}: {name} is {t.dtype}, not {dtype}")
@@ -457,6 +458,12 @@ def _buf(where, name, t, dtype, dev, need):
 
 def _span(t):
     return 1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())) if t.numel() else 0
+
+
+def _scratch(where, t, u8, dev):
+    """(address, bytes) of a scratch buffer."""
+    n = 1 if t is None else t.numel()
+    return _buf(where, "scratch", t, u8, dev, n), n
 
 
 def _where(stream, T):
@@ -535,7 +542,7 @@ def gpt2_op_prefix_attention_bf16(q, ldq, pk, pv, prefix_len, prefix_cap, k, v, 
                   _buf(f, "v", v, bf, dev, no), _buf(f, "len", len, T.i32, dev, B if max_len > 0 else 0), max_len,
                   _buf(f, "o", o, bf, dev, _extent(B, ldo, Hq * hd)), ldo,
                   None if lse is None else _buf(f, "lse", lse, T.f32, dev, B * Hq),
-                  _buf(f, "scratch", scratch, T.u8, dev, 1), scratch.numel(), B, Hq, Hkv, hd, st)
+                  *_scratch(f, scratch, T.u8, dev), B, Hq, Hkv, hd, st)
     if rc:
         raise Gpt2Error(rc, f)
 

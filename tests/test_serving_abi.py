@@ -132,3 +132,19 @@ def test_binding_refuses_host_short_and_mistyped_buffers(L):
         gp.LogitRules(history=torch.zeros(1, 2, dtype=torch.int32))
     with pytest.raises(gp.Gpt2Error, match="rules are for"):
         gp.LogitRules(presence=torch.zeros(2), frequency=torch.zeros(3))
+
+
+def test_binding_refuses_views_that_repeat_elements():
+    # an expanded tensor counts more elements than its memory holds
+    import torch
+    one = torch.zeros(1, dtype=torch.bfloat16)
+    with pytest.raises(gp.Gpt2Error, match="holds 1 elements, 64 are needed"):
+        gp._buf("f", "bias", one.expand(64), torch.bfloat16, -1, 64)
+    with pytest.raises(gp.Gpt2Error, match="holds 8 elements, 32 are needed"):
+        gp._buf("f", "x", torch.zeros(8).expand(4, 8), torch.float32, -1, 32)
+    rows = torch.zeros(4, 16)
+    assert gp._buf("f", "x", rows[:, :8], torch.float32, -1, 56) == rows.data_ptr()
+    assert gp._buf("f", "x", rows, torch.float32, -1, 64) == rows.data_ptr()
+    assert gp._buf("f", "x", rows.t(), torch.float32, -1, 64) == rows.data_ptr()
+    with pytest.raises(gp.Gpt2Error, match="scratch holds 1 elements, 4096 are needed"):
+        gp._scratch("f", torch.zeros(1, dtype=torch.uint8).expand(4096), torch.uint8, -1)
