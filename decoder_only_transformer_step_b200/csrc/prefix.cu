@@ -777,6 +777,7 @@ struct PrefixPlan {
 };
 bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan* p) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || P < 0 || max_len < 0) return false;
+  if (P > 1 << 30 || max_len > 1 << 30) return false;  // (the ends of parts stay inside 32 bits)
   if (hd != 16 && hd != 64 && hd != 128) return false;
   const int G = Hq / Hkv;
   const long M = (long)B * G;

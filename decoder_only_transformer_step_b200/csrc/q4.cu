@@ -1063,9 +1063,9 @@ int q4_run(Q4Args& a, int group, cudaStream_t st) {
   return q4_launch_rows(a, p, group, st);
 }
 
-// (K: at most 65535 k blocks of a grid)
+// (K: at most 65535 k blocks of a grid; N: the ends of tiles stay inside 32 bits)
 bool q4_shape_ok(int N, int K, int group) {
-  return K <= 65535 * QZ_K && (group == 32 || group == 64 || group == 128) && N >= 0 && K >= 1 && K % group == 0;
+  return K <= 65535 * QZ_K && (group == 32 || group == 64 || group == 128) && N >= 0 && N <= 1 << 30 && K >= 1 && K % group == 0;
 }
 
 }  // namespace

@@ -512,7 +512,7 @@ int gpt2_op_lm_head_ce_bwd_bf16(const uint16_t* x, const uint16_t* w, int M, int
  * holding q + 8 of inputs 2i (low half) and 2i + 1.  scales: bf16 [K / group]
  * rows of N rounded up to a multiple of 8 (the added columns are written 0).
  * A group that holds an infinity or NaN gets such a scale.  Matrix buffers are
- * 16-byte aligned. */
+ * 16-byte aligned.  N at most 2^30. */
 size_t gpt2_op_q4_packed_bytes(int N, int K);             /* 0 for invalid sizes */
 size_t gpt2_op_q4_scale_count(int N, int K, int group);   /* elements; 0 for invalid sizes */
 
@@ -545,7 +545,8 @@ int gpt2_op_gemv_q4(const uint16_t* x, int ldx, const uint8_t* packed, const uin
  * q, o bf16 [B, Hq * hd] with row pitches ldq, ldo (even, 4-byte aligned);
  * pk, pv bf16 [Hkv][prefix_cap][hd]; k, v bf16 [B][Hkv][max_len][hd] (16-byte
  * aligned); len device int32 [B], clamped to 0..max_len; lse fp32 [B, Hq] or
- * NULL.  hd 16, 64 or 128, Hq a multiple of Hkv.  prefix_len or max_len 0: that
+ * NULL.  hd 16, 64 or 128, Hq a multiple of Hkv, prefix_len and max_len at
+ * most 2^30.  prefix_len or max_len 0: that
  * part's pointers may be NULL.  A row without any key gets o = 0, lse = -inf.
  * Keys past prefix_len or len[b] are not read.  scratch: device, 16-byte
  * aligned, at least the given bytes (0 for invalid sizes); calls in flight at

@@ -148,3 +148,19 @@ def test_binding_refuses_views_that_repeat_elements():
     assert gp._buf("f", "x", rows.t(), torch.float32, -1, 64) == rows.data_ptr()
     with pytest.raises(gp.Gpt2Error, match="scratch holds 1 elements, 4096 are needed"):
         gp._scratch("f", torch.zeros(1, dtype=torch.uint8).expand(4096), torch.uint8, -1)
+
+
+def test_sizes_near_the_end_of_32_bits_are_refused(L):
+    # offsets of parts and tiles are formed from them by additions in 32 bits
+    big = 2**31 - 1
+    assert gp.gpt2_op_prefix_attention_scratch_bytes(1, 1, 1, 16, 2**30, 0) > 0
+    assert gp.gpt2_op_prefix_attention_scratch_bytes(1, 1, 1, 16, big, 0) == 0
+    assert gp.gpt2_op_prefix_attention_scratch_bytes(1, 1, 1, 16, 0, big) == 0
+    call = lambda P, m: L.gpt2_op_prefix_attention_bf16(  # noqa: E731
+        A, 16, A, A, P, big, A, A, A, m, A, 16, None, A, 1 << 40, 1, 1, 1, 16, None)
+    assert call(big, 0) == call(0, big) == SHAPE
+    assert gp.gpt2_op_q4_scale_count(2**30, 32, 32) > 0
+    assert gp.gpt2_op_q4_scale_count(big, 32, 32) == 0
+    assert L.gpt2_op_q4_quantize(A, 1, 32, big, 32, 32, A, A, None) == SHAPE
+    assert L.gpt2_op_q4_dequantize(A, A, big, 32, 32, A, 0, 32, None) == SHAPE
+    assert L.gpt2_op_gemv_q4(A, 32, A, A, None, A, 0, big, 1, big, 32, 32, None) == SHAPE
