@@ -118,7 +118,10 @@ template <int HD> constexpr int pa_smem() {
 // ones): half a step, 2^-8 relative at most, as the output's own rounding.
 // Where a row has few keys in all and the whole batch reads little (DIRECT), a
 // block takes all keys of its rows instead, those of the prefix and then their
-// own, and writes the output itself.
+// own, and writes the output itself: 3 rows, 12 heads, 200 + 64 keys of 64 in
+// 4.2 us (5.2 in parts and joined).  In parts, 16 rows, 12 heads, 3500 + 596 keys
+// take 9.8 us with the join, bound by the two kernels' waits for memory (28 % of
+// HBM, issue slots 28 % busy).
 template <int HD, typename QT, bool DIRECT>
 __global__ void __launch_bounds__(PA_WARPS * 32)
     prefix_part_kernel(const __grid_constant__ PrefixArgs a, bf16* __restrict__ out, long ldo, float* __restrict__ lse) {
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32)
 
 // ------------------------------------------------- many rows: tcgen05 ------
 // The prefix's parts where a key/value head has many query rows: the products
-// S = Q K^T (M 128, N 128) and O += P V on the 5th-generation tensor cores, so
+// S = Q K^T (M 128, N 64) and O += P V on the 5th-generation tensor cores, so
 // that up to 256 rows share one pass over the keys.  One block per (key range,
 // key/value head, row group):
 //   warp 0        TMA: K and V tiles of 128 keys, alternately, through a ring
@@ -364,10 +367,12 @@ __global__ void __launch_bounds__(PA_WARPS * 32)
 // A step is 64 keys.  Tensor memory of a tile: two buffers of S (64 fp32
 // columns), over which the step's bf16 probabilities P (32 columns) are
 // written once S has been read, and O (hd).  S of the next step is issued
-// before P V of this one, so that the softmax never waits for the tensor
-// cores.  A row rescales its O only when
-// its maximum grows by more than 2^8 (the probabilities are formed against the
-// older maximum, exact in the final O / l).  Warps without rows take no part.
+// before P V of this one, so that the softmax waits little for the tensor cores
+// (200 to 420 cycles a step).  A row rescales its O only when its maximum grows by more than 2^8 (the
+// probabilities are formed against the older maximum, exact in the final O /
+// l).  Warps without rows take no part.  160 rows over 32768 keys of 128, 8
+// heads: 46 us (37 % of HBM, tensor pipe 43 %), about 1950 cycles a step, of
+// which two softmax warps that share a scheduler take 1600 to 1690, one alone 950.
 // Every wait is bounded; after one that ran out the part's rows become NaN.
 constexpr float PT_RESCALE = 8.f;
 template <int HD> constexpr int pt_slots() { return HD == 128 ? 5 : 8; }
@@ -653,7 +658,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
 }
 
 // Joins the parts of a row (in the order of the parts): a block a row, its
-// warps take the parts in turn, a lane the same dims of each.
+// warps take the parts in turn, a lane the same dims of each.  Bound by the
+// waits for the parts: 6 us for 192 rows, 10 for 1280 of 128 dims (cold caches).
 template <int HD>
 __global__ void __launch_bounds__(128)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a, bf16* __restrict__ o, long ldo, float* __restrict__ lse) {

@@ -18,8 +18,9 @@ namespace {
 // A block takes 32 rows x 256 inputs: a lane holds 8 consecutive inputs of
 // each of the 4 rows of its warp (all loads in flight together), a group is
 // 4, 8 or 16 neighbouring lanes.  The scales of the tile meet in shared memory
-// and leave as runs of 32 columns.  Bound by HBM: 2 or 4 bytes a weight in,
-// half a byte out.
+// and leave as runs of 32 columns.  HBM asks for 2 or 4 bytes a weight in and
+// half a byte out, but the rounding takes longer: bf16, 50304 x 1600, groups of
+// 32: 69 us, 33 % of HBM, issue slots 75 % and ALU pipe 66 % busy.
 constexpr int QZ_ROWS = 32, QZ_K = 256;
 
 // q + 8 of eight weights as nibbles, q = clamp(rint(w / s), -7, 7) with the
@@ -157,7 +158,8 @@ DEVI uint32_t q4_sub136(uint32_t a) {
 // The values the nibbles stand for, s q (exact in fp32, rounded once to bf16
 // where T is bf16).  A warp takes 256 inputs of 8 rows, a lane 8 inputs of
 // each with all loads in flight together; the 64 rows of a block share the
-// sectors of the scales.
+// sectors of the scales.  Bound by HBM's latency and writes: bf16, 50304 x 1600:
+// 37 us, 52 % of HBM.
 constexpr int DQ_ROWS = 8;
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -222,12 +224,16 @@ __global__ void __launch_bounds__(256)
 // and x is staged in it.
 //
 // A block is 16 warps.  KS of them share a tile of 16 columns, each taking
-// every KS-th stage of 128 inputs; their sums meet in shared memory in a fixed
-// order.  Each warp copies its own stages (16 rows x 64 bytes and their
+// every KS-th stage of 256 inputs; their sums meet in shared memory in a fixed
+// order.  Each warp copies its own stages (16 rows x 128 bytes and their
 // scales) into a ring of its own with cp.async, several ahead, across tile
 // borders: no block-wide wait stands in the stream.  Inputs too long for
 // shared memory are split over the blocks of a cluster (up to 8), whose sums
 // meet through distributed shared memory, again in a fixed order.
+//
+// 8 x 50304 x 1600, groups of 32: 18 us (2.6 TB/s); 5 x 28673 x 8192, groups of
+// 128: 33 us (3.6 TB/s, 27.6 without the products): half the issue slots and
+// ALU cycles taken (48 and 51 %, 36 and 45 %), the rest waits of 16 warps.
 constexpr int Q4_WARPS = 16;
 constexpr int Q4_COLS = 16;                    // output columns of a tile (the mma M)
 constexpr int Q4_STAGE = 256;                  // inputs of a stage
@@ -763,7 +769,9 @@ __global__ void __launch_bounds__(Q4_WARPS * 32, 1) q4_gemv_kernel(const __grid_
 // packed subtraction of 136 / 1024 leaves two q / 1024 exactly (a group's sum
 // of up to 128 products |q| <= 8 then stays in range whatever x is; the scale
 // takes the 1024 back).  fp32 or LayerNorm'd rows are first
-// brought into shared memory as bf16 (STAGED; one warp a row).
+// brought into shared memory as bf16 (STAGED; one warp a row).  1 x 4800 x 1600
+// takes 4.9 us, 16 x 1600 x 6400 8.0: bound by waits for memory, at 16 rows by
+// every block's own reading of all of x.
 constexpr int QD_WARPS = 16;
 constexpr int QD_STAGED_K = 2048;  // widest staged row
 constexpr int QD_PAD = 32;         // elements behind a staged row: an odd multiple of 64 bytes in all

@@ -44,7 +44,10 @@ struct RulesArgs {
 // batch of logits is requested before that.  The pass over the slice only
 // masks, copies and compares; the few ids with a word are listed and left to a
 // second pass with a thread each, since in the first almost every warp would
-// take their path for one lane.
+// take their path for one lane.  384 x 50257 with histories of 4096 ids: 63 us
+// (logits in and out at 2.5 TB/s, issue slots 65 % busy), 42 without a history,
+// 36 without biases too, 27 without mask and choice as well; 16 x 50257: 7.2 us, one
+// round trip after the other.
 template <bool COUNTED, bool MASKED>
 __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_constant__ RulesArgs a) {
   extern __shared__ uint32_t rl_word[];  // [per] words, [n_bias] bias values, [list] ids
