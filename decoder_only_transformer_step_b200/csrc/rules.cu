@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
         if (e) t = __fadd_rn(t, bias[e - 1]);
         if (MASKED && !((allowed[i >> 5] >> (i & 31)) & 1u)) t = -INFINITY;
         out[i] = t;
-        if (greedy_better(t, v0 + i, bv, bi)) {
+        if (t != -INFINITY && greedy_better(t, v0 + i, bv, bi)) {  // (-inf is never chosen, as above)
           bv = t;
           bi = v0 + i;
         }

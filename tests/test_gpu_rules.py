@@ -188,3 +188,36 @@ def test_without_a_choice():
     assert torch.equal(z, out)                                       # no history: nothing to penalise
     with pytest.raises(gp.Gpt2Error):
         gp.gpt2_op_logit_rules(z, 500, out, 500, 4, 500, gp.LogitRules(presence=pres[:3].clone()))
+
+
+@pytest.mark.parametrize("rows", [6, 450])               # a row's 8 blocks, one block a row
+@pytest.mark.parametrize("parts", ["h", "b", "hgrpfb"])
+@pytest.mark.parametrize("append", [False, True])
+def test_nothing_left_beside_a_history_and_biases_is_id_0(rows, parts, append):
+    V = 2000
+    rng = np.random.default_rng(15)
+    z = rng.standard_normal((rows, V)).astype(F)
+    allowed = np.full((rows, (V + 31) // 32), -1, np.int32)
+    allowed[0::3] = 0                                     # the mask leaves nothing
+    z[1::3] = -np.inf                                     # the logits leave nothing; the other rows choose
+    r = dict(allowed=allowed)
+    if "h" in parts:
+        r["history"] = rng.integers(17, V, (rows, 40)).astype(np.int32)   # no id 0
+        r["history_len"] = rng.integers(5, 39, rows).astype(np.int32)
+    if "g" in parts:
+        r["gen_start"] = np.full(rows, 3, np.int32)
+        for k in ("repetition", "presence", "frequency"):
+            r[k] = (1 + rng.random(rows)).astype(F)
+    if "b" in parts:
+        r["bias_ids"] = rng.integers(17, V, (rows, 9)).astype(np.int32)
+        r["bias_values"] = rng.standard_normal((rows, 9)).astype(F)
+    append = append and "h" in parts
+    want, nxt = reference(z, V, r)
+    out, got, rules = run(z, V, r, append=append)
+    np.testing.assert_array_equal(out, want)
+    np.testing.assert_array_equal(got, nxt)
+    assert not got[0::3].any() and not got[1::3].any()
+    if append:
+        n = r["history_len"]
+        np.testing.assert_array_equal(rules.tensors["history_len"].cpu().numpy(), n + 1)
+        assert (rules.tensors["history"].cpu().numpy()[np.arange(rows), n] == nxt).all()
