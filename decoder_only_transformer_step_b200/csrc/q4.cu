@@ -211,8 +211,12 @@ __global__ void __launch_bounds__(256)
 // numbers and the lowest normal ones lie on one line), which mma takes
 // exactly, so that one AND leaves two operands (a nibble in the upper half of
 // a byte counts 16-fold).  To match, each row of x is staged times the power
-// of two that brings its largest magnitude to 2^60, a sixteenth of that at
-// odd k: exact in bf16, but for numbers below 2^-180 of the row's largest.
+// of two that brings its largest magnitude to 2^114, a sixteenth of that at
+// odd k: exact in bf16, but for numbers below 2^-234 of the row's largest.
+// So a row's sum is formed in a unit of at most 2^19 of its largest magnitude:
+// with |q| <= 8 and 2^15 inputs it stays below any scale's own bound (no sum
+// overflows that the result does not), and it is subnormal, off by up to
+// 2^-131 of that magnitude an addition, only where scales are below 2^-100.
 // The nibbles are q + 8, so a group's sum starts at -8 sum x instead of 0 (the
 // group sums of x are formed once, when x is staged).  A group's products are
 // summed in fp32 by the tensor core and multiplied by the group's scale in
@@ -427,11 +431,11 @@ DEVI void q4_stage_x(const Q4Args& a, bf16* xs, int xp, float2* fac, uint32_t* w
     m = __reduce_max_sync(0xffffffffu, m);
   }
   if (!live) return;
-  // 2^60 over the power of two at or below it (1 for a row of zeros, and for
+  // 2^114 over the power of two at or below it (1 for a row of zeros, and for
   // one that holds an infinity or NaN: its sums are not finite anyway), a
   // sixteenth of it in the upper halves, the odd inputs; in two steps where
   // that is above 2^127
-  const int ex = (int)(m >> 7), sh = m == 0 || ex == 255 ? 0 : 187 - ex, s1 = sh > 127 ? sh - 127 : 0, s2 = sh - s1;
+  const int ex = (int)(m >> 7), sh = m == 0 || ex == 255 ? 0 : 241 - ex, s1 = sh > 127 ? sh - 127 : 0, s2 = sh - s1;
   const uint32_t f1 = (uint32_t)(127 + s1) * 0x00800080u, f2 = (uint32_t)(127 + s2) << 7 | (uint32_t)(123 + s2) << 23;
   if (lane == 0 && part == 0) {
     const int un = 133 - sh;

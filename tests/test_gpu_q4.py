@@ -226,3 +226,30 @@ def test_rows_of_any_magnitude_and_rows_that_are_not_finite(N, K, group, rows):
     assert not bool(torch.isfinite(z[1:3]).any())
     keep = [r for r in range(rows) if r not in (1, 2)]
     assert torch.equal(z[keep], y[keep])
+
+
+@pytest.mark.parametrize("N,K,group", [(4200, 1536, 32), (2100, 5376, 64), (2100, 5376, 128)])  # streamed
+@pytest.mark.parametrize("rows", [1, 7, 16])
+@pytest.mark.parametrize("size", [-133, -126, -100, -70, -60, 60, 100, 118, 126])
+def test_scales_of_any_magnitude(N, K, group, rows, size):
+    # Scales near 2^size, x such that the results are ordinary numbers where x's range allows it.  An addition is
+    # off by at most a step (2^-23) of sum |s (|q| + 8) |x|| (the streamed form starts a group at -8 sum x) and, where
+    # the streamed form's sums are subnormal, by half of 2^-149 in its own unit, which is at most 2^19 max |x| of the row
+    rng = np.random.default_rng(1000 + N + size)
+    nib = rng.integers(0, 16, size=(N, K)).astype(np.uint8)
+    packed = torch.from_numpy(nib[:, 0::2] | (nib[:, 1::2] << 4)).cuda()
+    scales = torch.zeros(K // group, pitch(N), device="cuda").bfloat16()
+    one = 2.0 ** (size + rng.integers(-2 if size > -130 else 0, 2, (K // group, N)))
+    scales[:, :N] = torch.from_numpy(one).cuda()
+    x = torch.from_numpy(rng.standard_normal((rows, K)) * 2.0 ** np.clip(-size, -100, 100)).bfloat16().cuda()
+    y = torch.empty(rows, N, device="cuda")
+    gp.gpt2_op_gemv_q4(x, K, packed, scales, None, y, 1, N, rows, N, K, group)
+    s64 = scales[:, :N].double().t().repeat_interleave(group, 1)
+    q = torch.from_numpy(nib.astype(np.float64) - 8).cuda()
+    want, mag = x.double() @ (s64 * q).t(), x.double().abs() @ (s64 * (q.abs() + 8)).t()
+    depth = (group // 32) * 17 + K / group + 16 + 8 + 3
+    tol = depth * 2.0**-23 * mag + 2.0**-24 * want.abs() + depth * 2.0**-131 * x.double().abs().amax(1, keepdim=True) + 2.0**-148
+    assert bool(torch.isfinite(y).all())
+    assert bool(((y.double() - want).abs() <= tol).all()), float(((y.double() - want).abs() / tol).max())
+    if size >= -100:  # (the last two terms are the smallest part of it there)
+        assert bool((want.abs().amax(1) > 2.0**4 * tol.amax(1)).all())
