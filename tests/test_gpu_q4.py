@@ -228,7 +228,8 @@ def test_rows_of_any_magnitude_and_rows_that_are_not_finite(N, K, group, rows):
     assert torch.equal(z[keep], y[keep])
 
 
-@pytest.mark.parametrize("N,K,group", [(4200, 1536, 32), (2100, 5376, 64), (2100, 5376, 128)])  # streamed
+@pytest.mark.parametrize("N,K,group", [(100, 512, 64), (130, 1280, 32), (1500, 6400, 128),     # read directly
+                                       (4200, 1536, 32), (2100, 5376, 64), (2100, 5376, 128)])  # streamed
 @pytest.mark.parametrize("rows", [1, 7, 16])
 @pytest.mark.parametrize("size", [-133, -126, -100, -70, -60, 60, 100, 118, 126])
 def test_scales_of_any_magnitude(N, K, group, rows, size):
