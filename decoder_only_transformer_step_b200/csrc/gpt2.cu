@@ -946,7 +946,8 @@ int gpt2_decode_step_ex(gpt2_ctx* c, void* cache, size_t cache_bytes, int batch,
 int gpt2_rules_next(gpt2_ctx* c, float* logits, int batch, const gpt2_logit_rules* rules, int32_t* next_tokens,
                     int32_t* pos, void* stream) {
   if (!c || !logits || !rules || !next_tokens || batch < 1) return GPT2_ERR_INVALID_ARG;
-  return logit_rules(logits, c->s.V, logits, c->s.V, batch, (int)c->s.Vr, rules, next_tokens, pos, S(stream));
+  return logit_rules(logits, c->s.V, logits, c->s.V, batch, (int)c->s.Vr, rules, next_tokens, pos, c->w.err,
+                     S(stream));
 }
 
 int gpt2_prefill(gpt2_ctx* c, void* cache, size_t cache_bytes, int batch, int max_len, const int32_t* tokens,
@@ -1116,7 +1117,8 @@ int gpt2_set_wait_timeout_ns(uint64_t ns) {
   const unsigned long long v = ns ? (unsigned long long)ns : WAIT_TIMEOUT_NS;
   TRY(gemm_tc_set_wait_limit(v));
   TRY(attn_tc_set_wait_limit(v));
-  return prefix_set_wait_limit(v);
+  TRY(prefix_set_wait_limit(v));
+  return rules_set_wait_limit(v);
 }
 
 int gpt2_op_gemm_bf16_status(const uint16_t* A, int a_mn_major, int lda, const uint16_t* B, int b_mn_major, int ldb,

@@ -71,6 +71,7 @@ int num_sms();
 int gemm_tc_set_wait_limit(unsigned long long ns);
 int attn_tc_set_wait_limit(unsigned long long ns);
 int prefix_set_wait_limit(unsigned long long ns);
+int rules_set_wait_limit(unsigned long long ns);
 
 // tcgen05 causal attention forward / backward, head_dim 64 (bf16).  The
 // backward expects dvec = rowsum(dO * O) and a zeroed fp32 dq_acc; it writes dK,
@@ -233,6 +234,6 @@ int prefix_attention_f32(const float* q, const float* pk, const float* pv, int P
                          const float* v, const int32_t* len, int len_add, int max_len, int B, int H, int hd, float* o,
                          cudaStream_t st);
 
-// ---- rules on logits (see gpt2_op_logit_rules) ----------------------------
+// ---- rules on logits (see gpt2_op_logit_rules); err: device status word or NULL
 int logit_rules(const float* logits, long ld, float* out, long ldo, int rows, int vocab, const gpt2_logit_rules* r,
-                int32_t* next, int32_t* pos, cudaStream_t st);
+                int32_t* next, int32_t* pos, int* err, cudaStream_t st);

@@ -34,6 +34,7 @@ struct RulesArgs {
   int n_bias, list;   // list: room for the ids with a word (COUNTED)
   int32_t* next;
   int32_t* pos;
+  int* err;  // device status word or NULL
 };
 
 // One row's slice of ids.  Bound by the logits' way in and out of HBM at large
@@ -223,7 +224,8 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
       }
     // Ranks above 0 send (value, id) into rank 0's shared memory, counted on
     // its barrier: no fence waits for this block's stores to HBM, and the
-    // block may leave.
+    // block may leave.  A row whose blocks do not meet in time has no choice:
+    // id -1, which no later step takes for a token, and nothing moves on.
     if (rank > 0) {
       const uint64_t v = (uint64_t)(uint32_t)bi << 32 | __float_as_uint(bv);
       asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
@@ -234,7 +236,12 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
       if (a.split > 1) {
         const uint32_t bar = smem_u32(&arrived);
         mbar_arrive_expect_tx(bar, 8u * (a.split - 1));
-        mbar_drain_bounded(bar, 0);
+        int gave_up = 0;
+        if (!mbar_wait_bounded(bar, 0, &gave_up, a.err)) {
+          mbar_drain_bounded(bar, 0);  // (the others still send into this block's memory)
+          a.next[row] = -1;
+          return;
+        }
         for (int k = 1; k < a.split; ++k) {
           const uint64_t v = *reinterpret_cast<volatile uint64_t*>(&best[k]);
           const float ov = __uint_as_float((uint32_t)v);
@@ -286,8 +293,10 @@ bool bad_align(const void* p) { return ((uintptr_t)p & 3) != 0; }
 
 }  // namespace
 
+int rules_set_wait_limit(unsigned long long ns) { return set_unit_wait_limit(ns) == 0 ? GPT2_OK : GPT2_ERR_CUDA; }
+
 int logit_rules(const float* logits, long ld, float* out, long ldo, int rows, int vocab, const gpt2_logit_rules* r,
-                int32_t* next, int32_t* pos, cudaStream_t st) {
+                int32_t* next, int32_t* pos, int* err, cudaStream_t st) {
   if (!logits || !out || !r || rows < 0 || vocab < 0 || ld < vocab || ldo < vocab) return GPT2_ERR_INVALID_ARG;
   if (logits == out && ld != ldo) return GPT2_ERR_INVALID_ARG;
   if (pos && !next) return GPT2_ERR_INVALID_ARG;
@@ -304,7 +313,7 @@ int logit_rules(const float* logits, long ld, float* out, long ldo, int rows, in
     return GPT2_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0 || vocab == 0) return GPT2_OK;
   RulesArgs a = {};
-  a.z = logits; a.ld = ld; a.out = out; a.ldo = ldo; a.V = vocab; a.r = *r; a.next = next; a.pos = pos;
+  a.z = logits; a.ld = ld; a.out = out; a.ldo = ldo; a.V = vocab; a.r = *r; a.next = next; a.pos = pos; a.err = err;
   a.n_bias = r->n_bias;
   // blocks of a row: 8 while that fits the machine at once, and enough that
   // the words of six blocks fit an SM
@@ -323,7 +332,7 @@ extern "C" {
 
 int gpt2_op_logit_rules(const float* logits, int ld, float* out, int ldo, int rows, int vocab,
                         const gpt2_logit_rules* rules, int32_t* next, int32_t* pos, void* stream) {
-  return logit_rules(logits, ld, out, ldo, rows, vocab, rules, next, pos, reinterpret_cast<cudaStream_t>(stream));
+  return logit_rules(logits, ld, out, ldo, rows, vocab, rules, next, pos, nullptr, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -407,7 +407,10 @@ int gpt2_op_attention_bwd_bf16(const uint16_t* qkv, const uint16_t* o, const flo
  * and returns, so the context stays usable.  This sets the limit in
  * nanoseconds on the current device (0 restores the default of 2 s).  This
  * is the library's failure detection: a hung pipeline becomes an error the
- * host reads instead of a hung GPU.  Not stream-ordered: call it with no
+ * host reads instead of a hung GPU.  The blocks that choose an id under rules
+ * (gpt2_rules_next, gpt2_op_logit_rules) wait for one another the same way: a
+ * row for which that takes too long gets next id -1, its pos and history stay
+ * as they are, and gpt2_rules_next records the error.  Not stream-ordered: call it with no
  * kernel of the library in flight. */
 int gpt2_set_wait_timeout_ns(uint64_t ns);
 

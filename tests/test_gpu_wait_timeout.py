@@ -46,3 +46,44 @@ def test_timeout_is_reported_and_the_context_recovers(bn):
     assert int(status.item()) == 0
     ref = A.float() @ B.float().t()
     assert (C.float() - ref).abs().max().item() <= 1e-2 * ref.abs().max().item()
+
+
+def test_a_choice_whose_blocks_do_not_meet_in_time_is_no_token():
+    # 8 blocks share a row.  The whole history lies in the last one's ids, thousands of them and one again and again,
+    # so that block 0 has long been waiting when it reports; with the limit at one nanosecond it gives up.
+    rows, V, H = 4, 262144, 262143
+    g = torch.Generator().manual_seed(5)
+    z = torch.randn(rows, V, generator=g).cuda()
+    h = torch.full((rows, H), V - 1, dtype=torch.int32)
+    h[:, :H // 2] = torch.randint(7 * V // 8, V, (rows, H // 2), generator=g, dtype=torch.int32)
+    n0 = H - 1
+    hist, n = h.cuda(), torch.full((rows,), n0, dtype=torch.int32, device="cuda")
+    rules = gp.LogitRules(history=hist, history_len=n, presence=torch.ones(rows, device="cuda"), append=True)
+
+    def call():
+        out = torch.zeros(rows, V, device="cuda")
+        nxt = torch.full((rows,), -9, dtype=torch.int32, device="cuda")
+        pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+        n.fill_(n0)
+        hist[:, n0] = -7
+        gp.gpt2_op_logit_rules(z, V, out, V, rows, V, rules, nxt, pos)
+        torch.cuda.synchronize()
+        return out, nxt.tolist(), pos.tolist(), n.tolist(), hist[:, n0].tolist()
+    try:
+        gp.gpt2_set_wait_timeout_ns(1)
+        out, nxt, pos, length, last = call()
+    finally:
+        gp.gpt2_set_wait_timeout_ns(0)
+    out2, nxt2, pos2, length2, last2 = call()
+    want = z.clone()
+    for r in range(rows):
+        want[r, h[r, :n0].long().unique().cuda()] -= 1
+    assert torch.equal(out2, want) and torch.equal(out, want)     # the logits do not wait for one another
+    assert nxt2 == want.argmax(1).tolist() == last2
+    assert pos2 == [r + 1 for r in range(rows)] and length2 == [n0 + 1] * rows
+    assert -1 in nxt
+    for r in range(rows):
+        if nxt[r] == -1:
+            assert (pos[r], length[r], last[r]) == (r, n0, -7)
+        else:
+            assert (nxt[r], pos[r], length[r], last[r]) == (nxt2[r], r + 1, n0 + 1, nxt2[r])
