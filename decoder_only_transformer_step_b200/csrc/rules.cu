@@ -51,7 +51,7 @@ struct RulesArgs {
 // round trip after the other.
 template <bool COUNTED, bool MASKED>
 __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_constant__ RulesArgs a) {
-  extern __shared__ uint32_t rl_word[];  // [per] words, [n_bias] bias values, [list] ids
+  extern __shared__ __align__(16) uint32_t rl_word[];  // [per] words, [n_bias] bias values, [list] ids
   __shared__ float sv[RL_THREADS / 32];
   __shared__ int si[RL_THREADS / 32];
   __shared__ int listed;

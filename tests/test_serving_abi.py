@@ -164,3 +164,17 @@ def test_sizes_near_the_end_of_32_bits_are_refused(L):
     assert L.gpt2_op_q4_quantize(A, 1, 32, big, 32, 32, A, A, None) == SHAPE
     assert L.gpt2_op_q4_dequantize(A, A, big, 32, 32, A, 0, 32, None) == SHAPE
     assert L.gpt2_op_gemv_q4(A, 32, A, A, None, A, 0, big, 1, big, 32, 32, None) == SHAPE
+
+
+def test_shared_memory_accessed_in_wide_words_states_its_alignment():
+    # a misaligned 16-byte access would fault: the array's address must not hang on how large the static part is
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(gp.__file__), "csrc")
+    for name in ("q4.cu", "prefix.cu", "rules.cu"):
+        arrays = re.findall(r"extern __shared__ ([^;]*);", open(os.path.join(csrc, name)).read())
+        assert arrays
+        for a in arrays:
+            aligned = re.match(r"__align__\((\d+)\)", a)
+            # (smem_raw: its user rounds the address up to 1024 bytes)
+            assert a.endswith("smem_raw[]") or (aligned and int(aligned.group(1)) >= 16), (name, a)
