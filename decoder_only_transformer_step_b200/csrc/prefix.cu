@@ -458,21 +458,17 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       // ------------------------------------------------------------- TMA ----
       // tile 2 j is K of block j, tile 2 j + 1 its V
       int issued = 0;
-      bool ok = true;
       for (int i = 0; i < 2 * nb; ++i) {
         const int s = i % NS;
-        if (i >= NS && !mbar_wait_bounded(kv_empty(s), ((i - NS) / NS) & 1, abort_flag, nullptr)) {
-          ok = false;
-          break;
-        }
+        if (i >= NS && !mbar_wait_bounded(kv_empty(s), ((i - NS) / NS) & 1, abort_flag, nullptr)) break;
         mbar_arrive_expect_tx(kv_full(s), TB);
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c)
           tma_load_3d(kv_tile(s) + c * SUB, (i & 1) ? &tmV : &tmK, kv_full(s), 64 * c, k0 + (i >> 1) * 128, h);
         ++issued;
       }
-      if (!ok)
-        for (int i = issued - NS < 0 ? 0 : issued - NS; i < issued; ++i) mbar_drain_bounded(kv_full(i % NS), (i / NS) & 1);
+      // (all have landed, unless the others gave up: no copy may arrive after the block has left)
+      for (int i = issued - NS < 0 ? 0 : issued - NS; i < issued; ++i) mbar_drain_bounded(kv_full(i % NS), (i / NS) & 1);
     } else if ((warp == 1 || (NT == 2 && warp == 2)) && lane == 0 && rows_of(warp - 1) > 0) {
       // ------------------------------------------------------------- MMA ----
       const int t = warp - 1;
@@ -512,7 +508,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
         tc_commit(tbar(t, 5));
         if ((i & 1) || i + 1 == nh) tc_commit(kv_empty(s));
       }
-      if (!ok && issued) {
+      if (issued) {  // (whoever gave up: none of this warp's products is in flight when the tensor memory is freed)
         tc_commit(tbar(t, 6));
         mbar_drain_bounded(tbar(t, 6), 0);
       }

@@ -410,7 +410,8 @@ int gpt2_op_attention_bwd_bf16(const uint16_t* qkv, const uint16_t* o, const flo
  * host reads instead of a hung GPU.  The blocks that choose an id under rules
  * (gpt2_rules_next, gpt2_op_logit_rules) wait for one another the same way: a
  * row for which that takes too long gets next id -1, its pos and history stay
- * as they are, and gpt2_rules_next records the error.  Not stream-ordered: call it with no
+ * as they are, and gpt2_rules_next records the error.  The attention over a
+ * shared prefix, which has no status word, makes such rows NaN (o and lse).  Not stream-ordered: call it with no
  * kernel of the library in flight. */
 int gpt2_set_wait_timeout_ns(uint64_t ns);
 

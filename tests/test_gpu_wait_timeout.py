@@ -87,3 +87,40 @@ def test_a_choice_whose_blocks_do_not_meet_in_time_is_no_token():
             assert (pos[r], length[r], last[r]) == (r, n0, -7)
         else:
             assert (nxt[r], pos[r], length[r], last[r]) == (nxt2[r], r + 1, n0 + 1, nxt2[r])
+
+
+@pytest.mark.parametrize("hd,B", [(128, 256), (64, 100)])     # two row tiles, one
+def test_prefix_attention_whose_waits_run_out_is_nan_and_the_context_recovers(hd, B):
+    # the queries are read from pinned host memory: megabytes over the bus, for which the tensor cores' warps and the
+    # copies of the keys wait tens of microseconds
+    P = 40000 if hd == 128 else 60000
+    g = torch.Generator().manual_seed(hd)
+    q = torch.randn(B, hd, generator=g).bfloat16().pin_memory()
+    pk, pv = (torch.randn(1, P, hd, generator=g).bfloat16().cuda() for _ in range(2))
+    n = gp.gpt2_op_prefix_attention_scratch_bytes(B, 1, 1, hd, P, 0)
+    scratch = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def call(q):
+        o = torch.zeros(B, hd, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(B, 1, device="cuda")
+        torch.cuda.synchronize()
+        rc = gp._lib().gpt2_op_prefix_attention_bf16(q.data_ptr(), hd, pk.data_ptr(), pv.data_ptr(), P, P, None, None, None,
+                                                     0, o.data_ptr(), hd, lse.data_ptr(), scratch.data_ptr(), n, B, 1, 1,
+                                                     hd, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        return o, lse[:, 0]
+    o, lse = call(q.cuda())
+    try:
+        gp.gpt2_set_wait_timeout_ns(1)
+        o1, lse1 = call(q)
+    finally:
+        gp.gpt2_set_wait_timeout_ns(0)
+    gone = torch.isnan(lse1)
+    assert bool(gone.any())
+    assert bool(torch.isnan(o1[gone]).all())
+    assert torch.equal(o1[~gone], o[~gone]) and torch.equal(lse1[~gone], lse[~gone])
+    o2, lse2 = call(q)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    z = q.cuda().double() @ pk[0].double().t() / hd**0.5
+    assert bool(((o.double() - torch.softmax(z, 1) @ pv[0].double()).abs() <= 2e-2).all())
