@@ -91,18 +91,6 @@ template <> DEVI uint32_t ld_q2<float>(const float* p) {
   return pack_bf16x2(v.x, v.y);
 }
 
-// eight elements at a 16-byte boundary
-template <typename QT> DEVI void ld_q8(const QT* p, uint32_t (&w)[4]);
-template <> DEVI void ld_q8<bf16>(const bf16* p, uint32_t (&w)[4]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-}
-template <> DEVI void ld_q8<float>(const float* p, uint32_t (&w)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  w[0] = pack_bf16x2(a.x, a.y); w[1] = pack_bf16x2(a.z, a.w);
-  w[2] = pack_bf16x2(b.x, b.y); w[3] = pack_bf16x2(b.z, b.w);
-}
-
 template <int HD> constexpr int pa_smem() {
   constexpr int ring = PA_WARPS * PA_STAGES * 2 * pa_keys<HD>() * HD * 2, join = PA_WARPS * PA_ROWS * ((HD + 4) * 4 + 8);
   return ring > join ? ring : join;
@@ -397,7 +385,7 @@ __host__ __device__ inline int pt_rows(int n, int nt, int t) {
   return t == 0 ? min(r0, n) : n - min(r0, n);
 }
 
-template <int HD, int NT, typename QT>
+template <int HD, int NT>
 __global__ void __launch_bounds__(128 + 128 * NT, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PrefixArgs a) {
@@ -526,17 +514,20 @@ __global__ void __launch_bounds__(128 + 128 * NT, 1)
       const int m = m0 + (t ? rows_of(0) : 0) + (live ? lr : 0), b = m / a.G, hq = h * a.G + m % a.G;
       {
         // this thread's row of Q, K-major and 128-byte swizzled
-        const QT* src = reinterpret_cast<const QT*>(a.q) + (size_t)b * a.ldq + (size_t)hq * HD;
+        const bf16* src = reinterpret_cast<const bf16*>(a.q) + (size_t)b * a.ldq + (size_t)hq * HD;
         const uint32_t row = q_tile(t) + (uint32_t)at * 128u;
         uint32_t w[HD / 8][4];
         if (a.q_aligned) {
 #pragma unroll
-          for (int c = 0; c < HD / 8; ++c) ld_q8<QT>(src + 8 * c, w[c]);
+          for (int c = 0; c < HD / 8; ++c) {
+            const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * c);
+            w[c][0] = u.x; w[c][1] = u.y; w[c][2] = u.z; w[c][3] = u.w;
+          }
         } else {
 #pragma unroll
           for (int c = 0; c < HD / 8; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[c][e] = ld_q2<QT>(src + 8 * c + 2 * e);
+            for (int e = 0; e < 4; ++e) w[c][e] = ld_q2<bf16>(src + 8 * c + 2 * e);
         }
         // (the lanes without a row hold the group's first: finite, and dropped)
 #pragma unroll
@@ -818,17 +809,17 @@ bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan*
   return true;
 }
 
-template <int HD, int NT, typename QT>
+template <int HD, int NT>
 int prefix_tc_run(const PrefixArgs& a, cudaStream_t st) {
   CUtensorMap tk, tv;
   const uint64_t dims[3] = {HD, (uint64_t)a.P, (uint64_t)a.Hkv};
   const uint64_t strides[2] = {HD * 2, (uint64_t)a.pcap * HD * 2};
   if (!tmap_3d(&tk, a.pk, dims, strides) || !tmap_3d(&tv, a.pv, dims, strides)) return GPT2_ERR_CUDA;
-  CUDA_TRY(once_per_device((const void*)prefix_tc_kernel<HD, NT, QT>, [](int) {
-    return cudaFuncSetAttribute(prefix_tc_kernel<HD, NT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  CUDA_TRY(once_per_device((const void*)prefix_tc_kernel<HD, NT>, [](int) {
+    return cudaFuncSetAttribute(prefix_tc_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 pt_smem<HD, NT>());
   }));
-  CUDA_TRY(launch_k(prefix_tc_kernel<HD, NT, QT>, dim3((unsigned)(a.nsp * a.Hkv * a.mtp)), 128 + 128 * NT,
+  CUDA_TRY(launch_k(prefix_tc_kernel<HD, NT>, dim3((unsigned)(a.nsp * a.Hkv * a.mtp)), 128 + 128 * NT,
                     (size_t)pt_smem<HD, NT>(), st, tk, tv, a));
   LAUNCH_CHECK();
   return GPT2_OK;
@@ -858,9 +849,9 @@ int prefix_run(const PrefixArgs& a, bf16* o, long ldo, float* lse, cudaStream_t 
                       a, o, ldo, lse));
     LAUNCH_CHECK();
   }
-  if constexpr (HD >= 64) {
+  if constexpr (HD >= 64 && sizeof(QT) == 2) {
     if (a.tc) {
-      const int rc = (long)a.B * a.G <= 128 ? prefix_tc_run<HD, 1, QT>(a, st) : prefix_tc_run<HD, 2, QT>(a, st);
+      const int rc = (long)a.B * a.G <= 128 ? prefix_tc_run<HD, 1>(a, st) : prefix_tc_run<HD, 2>(a, st);
       if (rc != GPT2_OK) return rc;
     }
   }
@@ -879,6 +870,7 @@ size_t prefix_scratch_bytes(int B, int Hq, int Hkv, int hd, int P, int max_len) 
 int prefix_attention(const PrefixAttn& c, cudaStream_t st) {
   PrefixPlan p;
   if (!prefix_plan(c.B, c.Hq, c.Hkv, c.hd, c.P, c.max_len, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  if (c.q_f32 && p.tc) return GPT2_ERR_UNSUPPORTED_SHAPE;  // (a decode step has no 48 rows)
   if (c.scratch_bytes < p.bytes) return GPT2_ERR_WORKSPACE;
   PrefixArgs a = {};
   a.q = c.q; a.ldq = c.ldq; a.q_aligned = c.ldq % 8 == 0 && ((uintptr_t)c.q & 15) == 0;
