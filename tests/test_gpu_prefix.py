@@ -204,3 +204,35 @@ def test_a_cache_whose_offsets_pass_32_bits():
                                device="cuda")
     call(s)
     check(s)
+
+
+@pytest.mark.parametrize("hd,B,Hq,Hkv,P", [(64, 128, 12, 12, 16321), (64, 150, 24, 24, 16001), (64, 64, 75, 75, 22001),
+                                           (64, 25, 150, 30, 12001), (64, 257, 20, 20, 5601),
+                                           (128, 50, 37, 37, 14999), (128, 130, 40, 40, 6001), (128, 300, 25, 25, 2500),
+                                           (128, 24, 150, 75, 15000)])
+def test_long_parts_on_the_tensor_cores(hd, B, Hq, Hkv, P):
+    # so many key/value heads that a block takes 1024 keys and more: 20 to 344 steps, the ring of tiles used again and
+    # again; one row tile and two, several row groups, odd and even numbers of steps, a last step of any length
+    s = make(B, Hq, Hkv, hd, P, 3, [b % 4 for b in range(B)], seed=P + B, cap=P + 1, ldq=Hq * hd + (B % 2) * 2)
+    s["pk"][:, P:] = float("nan")
+    s["pv"][:, P:] = float("inf")
+    call(s)
+    check(s)
+
+
+@pytest.mark.parametrize("hd,B,P", [(128, 128, 5633), (128, 256, 2817), (64, 128, 11001), (64, 200, 7100)])
+@pytest.mark.parametrize("grow", [3.0, 9.0, 20.0])
+def test_maxima_that_grow_at_every_step_of_long_parts(hd, B, P, grow):
+    # one block a head takes the whole prefix.  The scores of the even rows grow by a factor 2^grow a step of 64 keys
+    # (above 2^8 every step rescales what came before, below it every few steps), those of the odd rows fall
+    H = 75
+    s = make(B, H, H, hd, P, 0, [0] * B, seed=B + P)
+    u = torch.where(torch.arange(hd, device="cuda") % 3 == 0, -1.0, 1.0)
+    top = grow * math.log(2) * P / 64                              # the largest score
+    c = math.sqrt(top / math.sqrt(hd))
+    sign = torch.where(torch.arange(B, device="cuda") % 2 == 0, 1.0, -1.0)
+    s["q"] = (sign[:, None, None] * c * u + 0.1 * s["q"].float().view(B, H, hd)).bfloat16().view(B, H * hd)
+    ramp = torch.linspace(0.0, c, P, device="cuda")
+    s["pk"] = (ramp[None, :, None] * u + 0.1 * s["pk"].float()).bfloat16()
+    call(s)
+    check(s)
