@@ -411,7 +411,8 @@ def gpt2_op_gemm_bf16_status(A, a_mn, lda, B, b_mn, ldb, C, c_fp32, ldc, M, N, K
 # ---- 4-bit weights, shared prefixes, rules on logits ------------------------
 # These calls know every buffer's extent, so they check it here: a buffer that
 # is too short, of another type or on another device is GPT2_ERR_INVALID_ARG
-# instead of a read out of range.  A decode step makes several of them in a few
+# instead of a read out of range, and so is a view whose elements do not lie
+# where the call looks for them (a transposed weight).  A decode step makes several of them in a few
 # microseconds of device time, so the checks are kept to what they need.
 
 _T = None  # what these calls use of torch and of the library, looked up once
@@ -439,16 +440,22 @@ def _torch():
     return _T
 
 
-def _buf(where, name, t, dtype, dev, need):
+def _buf(where, name, t, dtype, dev, need, pitch=None):
     """Address of a buffer on device `dev` of at least `need` elements (of a
     strided view: the memory from its first to its last one, which an expanded
-    tensor has less of than elements); None for None where none are needed."""
+    tensor has less of than elements); None for None where none are needed.
+    pitch: how far apart the call's rows lie, which a view has to share (0: the
+    call has no pitch, and a view has to be contiguous)."""
     if t is None:
         if need <= 0:
             return None
         raise Gpt2Error(-1, f"{where}: {name} is missing")
-    if t.dtype is dtype and t.get_device() == dev and (t.numel() if t.is_contiguous() else _span(t)) >= need:
-        return t.data_ptr()
+    whole = t.is_contiguous()
+    if t.dtype is dtype and t.get_device() == dev and (t.numel() if whole else _span(t)) >= need:
+        if whole or pitch is None or (t.stride(0) == pitch and t[0].is_contiguous()):
+            return t.data_ptr()
+        raise Gpt2Error(-1, f"{where}: {name} is a view with strides {t.stride()}, the call reads " +
+                        (f"rows {pitch} apart" if pitch else "its elements one behind the other"))
     if t.dtype is not dtype:
         raise Gpt2Error(-1, f"{where}: {name} is {t.dtype}, not {dtype}")
     if t.get_device() != dev:
@@ -494,9 +501,9 @@ def gpt2_op_q4_quantize(w, w_fp32, ldw, N, K, group, packed, scales, stream=None
     """w [N, ldw] bf16 (or fp32 with w_fp32) -> packed uint8 [N, K/2], scales bf16 [K/group, N up to a multiple of 8]."""
     T, f = _T or _torch(), "gpt2_op_q4_quantize"
     dev, st = _where(stream, T)
-    rc = T.quantize(_buf(f, "w", w, T.f32 if w_fp32 else T.bf16, dev, _extent(N, ldw, K)), w_fp32, ldw, N, K, group,
-                    _buf(f, "packed", packed, T.u8, dev, N * K // 2),
-                    _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), st)
+    rc = T.quantize(_buf(f, "w", w, T.f32 if w_fp32 else T.bf16, dev, _extent(N, ldw, K), ldw), w_fp32, ldw, N, K, group,
+                    _buf(f, "packed", packed, T.u8, dev, N * K // 2, 0),
+                    _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0, 0), st)
     if rc:
         raise Gpt2Error(rc, f)
 
@@ -504,9 +511,9 @@ def gpt2_op_q4_quantize(w, w_fp32, ldw, N, K, group, packed, scales, stream=None
 def gpt2_op_q4_dequantize(packed, scales, N, K, group, out, out_fp32, ldo, stream=None):
     T, f = _T or _torch(), "gpt2_op_q4_dequantize"
     dev, st = _where(stream, T)
-    rc = T.dequantize(_buf(f, "packed", packed, T.u8, dev, N * K // 2),
-                      _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0), N, K,
-                      group, _buf(f, "out", out, T.f32 if out_fp32 else T.bf16, dev, _extent(N, ldo, K)), out_fp32, ldo, st)
+    rc = T.dequantize(_buf(f, "packed", packed, T.u8, dev, N * K // 2, 0),
+                      _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0, 0), N, K,
+                      group, _buf(f, "out", out, T.f32 if out_fp32 else T.bf16, dev, _extent(N, ldo, K), ldo), out_fp32, ldo, st)
     if rc:
         raise Gpt2Error(rc, f)
 
@@ -515,10 +522,10 @@ def gpt2_op_gemv_q4(x, ldx, packed, scales, bias, out, out_fp32, ldo, rows, N, K
     """out [rows, ldo] = x [rows, ldx] W^T (+ bias) with W's 4-bit form; rows 1..16."""
     T, f = _T or _torch(), "gpt2_op_gemv_q4"
     dev, st = _where(stream, T)
-    rc = T.gemv(_buf(f, "x", x, T.bf16, dev, _extent(rows, ldx, K)), ldx, _buf(f, "packed", packed, T.u8, dev, N * K // 2),
-                _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0),
-                None if bias is None else _buf(f, "bias", bias, T.bf16, dev, N),
-                _buf(f, "out", out, T.f32 if out_fp32 else T.bf16, dev, _extent(rows, ldo, N)), out_fp32, ldo, rows, N, K,
+    rc = T.gemv(_buf(f, "x", x, T.bf16, dev, _extent(rows, ldx, K), ldx), ldx, _buf(f, "packed", packed, T.u8, dev, N * K // 2, 0),
+                _buf(f, "scales", scales, T.bf16, dev, K // group * ((N + 7) // 8 * 8) if group > 0 else 0, 0),
+                None if bias is None else _buf(f, "bias", bias, T.bf16, dev, N, 0),
+                _buf(f, "out", out, T.f32 if out_fp32 else T.bf16, dev, _extent(rows, ldo, N), ldo), out_fp32, ldo, rows, N, K,
                 group, st)
     if rc:
         raise Gpt2Error(rc, f)
@@ -537,11 +544,11 @@ def gpt2_op_prefix_attention_bf16(q, ldq, pk, pv, prefix_len, prefix_cap, k, v, 
     np = _extent(Hkv, prefix_cap * hd, prefix_len * hd)
     no = B * Hkv * max_len * hd
     bf = T.bf16
-    rc = T.prefix(_buf(f, "q", q, bf, dev, _extent(B, ldq, Hq * hd)), ldq, _buf(f, "pk", pk, bf, dev, np),
-                  _buf(f, "pv", pv, bf, dev, np), prefix_len, prefix_cap, _buf(f, "k", k, bf, dev, no),
-                  _buf(f, "v", v, bf, dev, no), _buf(f, "len", len, T.i32, dev, B if max_len > 0 else 0), max_len,
-                  _buf(f, "o", o, bf, dev, _extent(B, ldo, Hq * hd)), ldo,
-                  None if lse is None else _buf(f, "lse", lse, T.f32, dev, B * Hq),
+    rc = T.prefix(_buf(f, "q", q, bf, dev, _extent(B, ldq, Hq * hd), ldq), ldq, _buf(f, "pk", pk, bf, dev, np, prefix_cap * hd),
+                  _buf(f, "pv", pv, bf, dev, np, prefix_cap * hd), prefix_len, prefix_cap, _buf(f, "k", k, bf, dev, no, 0),
+                  _buf(f, "v", v, bf, dev, no, 0), _buf(f, "len", len, T.i32, dev, B if max_len > 0 else 0, 0), max_len,
+                  _buf(f, "o", o, bf, dev, _extent(B, ldo, Hq * hd), ldo), ldo,
+                  None if lse is None else _buf(f, "lse", lse, T.f32, dev, B * Hq, 0),
                   *_scratch(f, scratch, T.u8, dev), B, Hq, Hkv, hd, st)
     if rc:
         raise Gpt2Error(rc, f)
@@ -601,10 +608,10 @@ def gpt2_op_logit_rules(logits, ld, out, ldo, rows, vocab, rules, next_tokens=No
     """out [rows, ldo] = logits [rows, ld] under `rules` (a LogitRules); next_tokens: the greedy choice."""
     T, f = _T or _torch(), "gpt2_op_logit_rules"
     dev, st = _where(stream, T)
-    rc = T.rules(_buf(f, "logits", logits, T.f32, dev, _extent(rows, ld, vocab)), ld,
-                 _buf(f, "out", out, T.f32, dev, _extent(rows, ldo, vocab)), ldo, rows, vocab, _rules(f, rules, rows, dev),
-                 None if next_tokens is None else _buf(f, "next_tokens", next_tokens, T.i32, dev, rows),
-                 None if pos is None else _buf(f, "pos", pos, T.i32, dev, rows), st)
+    rc = T.rules(_buf(f, "logits", logits, T.f32, dev, _extent(rows, ld, vocab), ld), ld,
+                 _buf(f, "out", out, T.f32, dev, _extent(rows, ldo, vocab), ldo), ldo, rows, vocab, _rules(f, rules, rows, dev),
+                 None if next_tokens is None else _buf(f, "next_tokens", next_tokens, T.i32, dev, rows, 0),
+                 None if pos is None else _buf(f, "pos", pos, T.i32, dev, rows, 0), st)
     if rc:
         raise Gpt2Error(rc, f)
 

@@ -178,3 +178,72 @@ def test_shared_memory_accessed_in_wide_words_states_its_alignment():
             aligned = re.match(r"__align__\((\d+)\)", a)
             # (smem_raw: its user rounds the address up to 1024 bytes)
             assert a.endswith("smem_raw[]") or (aligned and int(aligned.group(1)) >= 16), (name, a)
+
+
+def test_binding_refuses_views_whose_elements_lie_elsewhere(monkeypatch):
+    import torch
+    # host tensors pass for the current device's, and no call leaves the binding
+    calls = []
+    T = gp._torch()
+    for name in ("quantize", "dequantize", "gemv", "prefix", "rules"):
+        monkeypatch.setattr(T, name, lambda *a: calls.append(a) or 0)
+    monkeypatch.setattr(gp, "_where", lambda *a: (-1, None))
+    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    N, K, g, rows = 8, 64, 32, 4
+    ok = dict(x=torch.zeros(rows, K, dtype=bf), w=torch.zeros(N, K), packed=torch.zeros(N, K // 2, dtype=u8),
+              scales=torch.zeros(K // g, N, dtype=bf), bias=torch.zeros(N, dtype=bf), out=torch.zeros(rows, N, dtype=bf),
+              deq=torch.zeros(N, K, dtype=bf))
+
+    def gemv(ldx=K, ldo=N, **kw):
+        a = {**ok, **kw}
+        gp.gpt2_op_gemv_q4(a["x"], ldx, a["packed"], a["scales"], a["bias"], a["out"], 0, ldo, rows, N, K, g)
+
+    def quantize(ldw=K, **kw):
+        a = {**ok, **kw}
+        gp.gpt2_op_q4_quantize(a["w"], 1, ldw, N, K, g, a["packed"], a["scales"])
+
+    def dequantize(ldo=K, **kw):
+        a = {**ok, **kw}
+        gp.gpt2_op_q4_dequantize(a["packed"], a["scales"], N, K, g, a["deq"], 0, ldo)
+
+    B, H, hd, P, cap, M = 2, 3, 16, 5, 9, 4
+    at = dict(q=torch.zeros(B, H, hd, dtype=bf), pk=torch.zeros(H, cap, hd, dtype=bf), k=torch.zeros(B, H, M, hd, dtype=bf),
+              v=torch.zeros(B, H, M, hd, dtype=bf), len=torch.zeros(B, dtype=i32), o=torch.zeros(B, H, hd, dtype=bf),
+              lse=torch.zeros(B, H), s=torch.zeros(1 << 16, dtype=u8))
+
+    def prefix(ldq=H * hd, ldo=H * hd, **kw):
+        a = {**at, **kw}
+        gp.gpt2_op_prefix_attention_bf16(a["q"], ldq, a["pk"], a["pk"], P, cap, a["k"], a["v"], a["len"], M, a["o"], ldo,
+                                         a["lse"], a["s"], B, H, H, hd)
+
+    z = torch.zeros(4, 100)
+
+    def rules(logits=z, out=z, ld=100, nxt=torch.zeros(4, dtype=i32), pos=None):
+        gp.gpt2_op_logit_rules(logits, ld, out, ld, 4, 100, gp.LogitRules(), nxt, pos)
+
+    wide = torch.zeros(rows, 2 * K, dtype=bf)
+    good = [lambda: gemv(), lambda: gemv(x=wide[:, :K], ldx=2 * K), lambda: gemv(x=wide.view(-1)), lambda: quantize(),
+            lambda: quantize(w=torch.zeros(N, K + 8)[:, :K], ldw=K + 8), lambda: dequantize(), lambda: prefix(),
+            lambda: prefix(pk=at["pk"][:, :P]), lambda: prefix(q=torch.zeros(B, 50, dtype=bf)[:, :48], ldq=50),
+            lambda: rules(), lambda: rules(logits=torch.zeros(4, 128)[:, :100], out=torch.zeros(4, 128), ld=128)]
+    for i, f in enumerate(good):
+        f()
+        assert len(calls) == i + 1
+    bad = [lambda: gemv(x=torch.zeros(K, rows, dtype=bf).t()),                       # transposed
+           lambda: gemv(x=wide[:, :K]),                                              # another pitch
+           lambda: gemv(x=wide[:, ::2]), lambda: gemv(packed=torch.zeros(K // 2, N, dtype=u8).t()),
+           lambda: gemv(packed=torch.zeros(N, K, dtype=u8)[:, :K // 2]),
+           lambda: gemv(scales=torch.zeros(N, K // g, dtype=bf).t()), lambda: gemv(bias=torch.zeros(N, 2, dtype=bf)[:, 0]),
+           lambda: gemv(out=torch.zeros(N, rows, dtype=bf).t()), lambda: quantize(w=torch.zeros(K, N).t()),
+           lambda: quantize(w=torch.zeros(2 * N, K)[::2]), lambda: dequantize(deq=torch.zeros(K, N, dtype=bf).t()),
+           lambda: prefix(q=torch.zeros(H, B, hd, dtype=bf).transpose(0, 1)),
+           lambda: prefix(pk=torch.zeros(cap, H, hd, dtype=bf).transpose(0, 1)),     # positions before heads
+           lambda: prefix(k=torch.zeros(B, M, H, hd, dtype=bf).transpose(1, 2)),
+           lambda: prefix(v=torch.zeros(B, H, 2 * M, hd, dtype=bf)[:, :, :M]),       # a longer cache's first positions
+           lambda: prefix(len=torch.zeros(2 * B, dtype=i32)[::2]), lambda: prefix(lse=torch.zeros(H, B).t()),
+           lambda: rules(logits=torch.zeros(100, 4).t()), lambda: rules(out=torch.zeros(4, 200)[:, ::2]),
+           lambda: rules(nxt=torch.zeros(8, dtype=i32)[::2]), lambda: rules(pos=torch.zeros(8, dtype=i32)[::2])]
+    for f in bad:
+        with pytest.raises(gp.Gpt2Error, match="is a view with strides"):
+            f()
+    assert len(calls) == len(good)
