@@ -924,7 +924,7 @@ int gpt2_op_prefix_attention_bf16(const uint16_t* q, int ldq, const uint16_t* pk
                                   int Hkv, int hd, void* stream) {
   if (B < 0 || Hq < 1 || Hkv < 1 || prefix_len < 0 || prefix_cap < prefix_len || max_len < 0)
     return GPT2_ERR_INVALID_ARG;
-  if (!q || !o || !scratch || (prefix_len && (!pk || !pv)) || (max_len && (!k || !v || !len)))
+  if (B && (!q || !o || !scratch || (prefix_len && (!pk || !pv)) || (max_len && (!k || !v || !len))))
     return GPT2_ERR_INVALID_ARG;
   if (((uintptr_t)q | (uintptr_t)o | (uintptr_t)lse | (uintptr_t)len) & 3) return GPT2_ERR_INVALID_ARG;
   if ((((uintptr_t)pk | (uintptr_t)pv) & 15 && prefix_len) || (((uintptr_t)k | (uintptr_t)v) & 15 && max_len))

@@ -1143,7 +1143,7 @@ size_t gpt2_op_q4_scale_count(int N, int K, int group) {
 
 int gpt2_op_q4_quantize(const void* w, int w_fp32, int ldw, int N, int K, int group, uint8_t* packed,
                         uint16_t* scales, void* stream) {
-  if (!w || !packed || !scales || N < 0 || K < 0 || ldw < K) return GPT2_ERR_INVALID_ARG;
+  if (N < 0 || K < 0 || ldw < K || (N && (!w || !packed || !scales))) return GPT2_ERR_INVALID_ARG;
   if (((uintptr_t)w | (uintptr_t)packed | (uintptr_t)scales) & 15) return GPT2_ERR_INVALID_ARG;
   if (!q4_shape_ok(N, K, group) || ldw % 8) return GPT2_ERR_UNSUPPORTED_SHAPE;
   if (N == 0) return GPT2_OK;
@@ -1152,7 +1152,7 @@ int gpt2_op_q4_quantize(const void* w, int w_fp32, int ldw, int N, int K, int gr
 
 int gpt2_op_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int N, int K, int group, void* out,
                           int out_fp32, int ldo, void* stream) {
-  if (!packed || !scales || !out || N < 0 || K < 0 || ldo < K) return GPT2_ERR_INVALID_ARG;
+  if (N < 0 || K < 0 || ldo < K || (N && (!packed || !scales || !out))) return GPT2_ERR_INVALID_ARG;
   if (((uintptr_t)packed | (uintptr_t)scales | (uintptr_t)out) & 15) return GPT2_ERR_INVALID_ARG;
   if (!q4_shape_ok(N, K, group) || ldo % 8) return GPT2_ERR_UNSUPPORTED_SHAPE;
   if (N == 0) return GPT2_OK;
@@ -1173,8 +1173,8 @@ int gpt2_op_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int N, 
 
 int gpt2_op_gemv_q4(const uint16_t* x, int ldx, const uint8_t* packed, const uint16_t* scales, const uint16_t* bias,
                     void* out, int out_fp32, int ldo, int rows, int N, int K, int group, void* stream) {
-  if (!x || !packed || !scales || !out || rows < 0 || rows > 16 || N < 0 || K < 0 || ldx < K || ldo < N)
-    return GPT2_ERR_INVALID_ARG;
+  if (rows < 0 || rows > 16 || N < 0 || K < 0 || ldx < K || ldo < N) return GPT2_ERR_INVALID_ARG;
+  if (rows && N && (!x || !packed || !scales || !out)) return GPT2_ERR_INVALID_ARG;
   if ((((uintptr_t)x | (uintptr_t)packed | (uintptr_t)scales) & 15) || ((uintptr_t)bias & 1) ||
       ((uintptr_t)out & (out_fp32 ? 3 : 1)))
     return GPT2_ERR_INVALID_ARG;

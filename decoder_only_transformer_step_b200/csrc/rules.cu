@@ -297,12 +297,13 @@ int rules_set_wait_limit(unsigned long long ns) { return set_unit_wait_limit(ns)
 
 int logit_rules(const float* logits, long ld, float* out, long ldo, int rows, int vocab, const gpt2_logit_rules* r,
                 int32_t* next, int32_t* pos, int* err, cudaStream_t st) {
-  if (!logits || !out || !r || rows < 0 || vocab < 0 || ld < vocab || ldo < vocab) return GPT2_ERR_INVALID_ARG;
-  if (logits == out && ld != ldo) return GPT2_ERR_INVALID_ARG;
+  if (!r || rows < 0 || vocab < 0 || ld < vocab || ldo < vocab) return GPT2_ERR_INVALID_ARG;
+  const bool any = rows && vocab;  // (an empty tensor's address is NULL)
+  if (any && (!logits || !out || (logits == out && ld != ldo))) return GPT2_ERR_INVALID_ARG;
   if (pos && !next) return GPT2_ERR_INVALID_ARG;
   if (r->history && (!r->history_len || r->history_ld < 1)) return GPT2_ERR_INVALID_ARG;
-  if (r->append && (!r->history || !next)) return GPT2_ERR_INVALID_ARG;
-  if (r->n_bias < 0 || (r->n_bias && (!r->bias_ids || !r->bias_values))) return GPT2_ERR_INVALID_ARG;
+  if (r->append && any && (!r->history || !next)) return GPT2_ERR_INVALID_ARG;
+  if (r->n_bias < 0 || (r->n_bias && any && (!r->bias_ids || !r->bias_values))) return GPT2_ERR_INVALID_ARG;
   if (r->allowed && r->allowed_ld < (vocab + 31) / 32) return GPT2_ERR_INVALID_ARG;
   if (bad_align(logits) || bad_align(out) || bad_align(r->history) || bad_align(r->history_len) ||
       bad_align(r->gen_start) || bad_align(r->repetition) || bad_align(r->presence) || bad_align(r->frequency) ||

@@ -247,3 +247,18 @@ def test_binding_refuses_views_whose_elements_lie_elsewhere(monkeypatch):
         with pytest.raises(gp.Gpt2Error, match="is a view with strides"):
             f()
     assert len(calls) == len(good)
+
+
+def test_calls_with_nothing_to_do_take_the_null_of_empty_tensors(L):
+    # (an empty tensor's address is NULL; sizes that are wrong stay wrong)
+    q = lambda N, K=64, ldw=64: L.gpt2_op_q4_quantize(None, 1, ldw, N, K, 32, None, None, None)  # noqa: E731
+    d = lambda N: L.gpt2_op_q4_dequantize(None, None, N, 64, 32, None, 0, 64, None)  # noqa: E731
+    assert q(0) == d(0) == 0 and q(1) == d(1) == q(0, ldw=32) == INVALID and q(0, K=48) == SHAPE
+    g = lambda rows, N, K=64: L.gpt2_op_gemv_q4(None, 64, None, None, None, None, 0, 8, rows, N, K, 32, None)  # noqa: E731
+    assert g(0, 8) == g(2, 0) == 0 and g(1, 1) == g(17, 0) == INVALID and g(0, 8, K=48) == SHAPE
+    p = lambda B, hd=64: L.gpt2_op_prefix_attention_bf16(  # noqa: E731
+        None, 256, None, None, 8, 8, None, None, None, 4, None, 256, None, None, 0, B, 4, 4, hd, None)
+    assert p(0) == 0 and p(1) == INVALID and p(0, hd=32) == SHAPE
+    r = lambda rows, V, **k: L.gpt2_op_logit_rules(  # noqa: E731
+        None, 100, None, 100, rows, V, ctypes.byref(gp.gpt2_logit_rules(**k)), None, None, None)
+    assert r(0, 100) == r(2, 0) == r(0, 100, n_bias=3) == r(0, 100, append=1) == 0 and r(2, 100) == INVALID
