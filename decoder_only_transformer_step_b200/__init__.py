@@ -561,7 +561,7 @@ class LogitRules:
     gen_start int32 [rows]; repetition, presence, frequency fp32 [rows];
     bias_ids int32 and bias_values fp32 [rows, n]; allowed int32 or uint32
     [rows, words], bit v % 32 of word v // 32 set where id v may be chosen;
-    append: the chosen id is added to the history.  The tensors stay the
+    append: the chosen id is added to the history where there is room.  The tensors stay the
     caller's and are read at every call, so they can be changed in between."""
 
     def __init__(self, history=None, history_len=None, gen_start=None, repetition=None, presence=None, frequency=None,
@@ -588,13 +588,15 @@ class LogitRules:
             raise Gpt2Error(-1, f"{f}: the rules are not on a CUDA device")
 
         def at(name, dtype):
-            return _buf(f, name, self.tensors[name], dtype, dev, 0)
+            a = _buf(f, name, self.tensors[name], dtype, dev, 0)
+            return a if width.get(name, 1) else None  # (a table of no columns is none)
         words = T.words[0] if allowed is None or allowed.dtype is T.words[0] else T.words[1]
         self.device = dev
         self.c = gpt2_logit_rules(
             at("history", T.i32), at("history_len", T.i32), at("gen_start", T.i32), at("repetition", T.f32),
             at("presence", T.f32), at("frequency", T.f32), at("bias_ids", T.i32), at("bias_values", T.f32),
-            at("allowed", words), width["history"], width["bias_ids"], width["allowed"], int(append))
+            at("allowed", words), width["history"], width["bias_ids"], width["allowed"],
+            int(append and (history is None or width["history"] > 0)))
         self._ref = ctypes.byref(self.c)
 
 

@@ -262,3 +262,20 @@ def test_calls_with_nothing_to_do_take_the_null_of_empty_tensors(L):
     r = lambda rows, V, **k: L.gpt2_op_logit_rules(  # noqa: E731
         None, 100, None, 100, rows, V, ctypes.byref(gp.gpt2_logit_rules(**k)), None, None, None)
     assert r(0, 100) == r(2, 0) == r(0, 100, n_bias=3) == r(0, 100, append=1) == 0 and r(2, 100) == INVALID
+
+
+def test_a_history_without_room_is_none(monkeypatch):
+    # also as a view, whose address is not NULL: nothing counts and nothing is added
+    import torch
+    monkeypatch.setattr(gp, "_buf", lambda where, name, t, *a: None if t is None else t.data_ptr() or None)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    n = torch.zeros(3, dtype=torch.int32)
+    for h in (torch.zeros(3, 0, dtype=torch.int32), torch.zeros(3, 8, dtype=torch.int32)[:, 4:4]):
+        r = gp.LogitRules(history=h, history_len=n, presence=torch.ones(3), append=True)
+        assert r.c.history is None and r.c.history_ld == 0 and r.c.append == 0 and r.rows == 3
+    r = gp.LogitRules(history=torch.zeros(3, 8, dtype=torch.int32), history_len=n, append=True)
+    assert r.c.history and r.c.history_ld == 8 and r.c.append == 1
+    b = torch.zeros(3, 4)[:, 2:2]
+    r = gp.LogitRules(bias_ids=b.int(), bias_values=b)
+    assert r.c.bias_values is None and r.c.n_bias == 0
+    assert gp.LogitRules(append=True).c.append == 1      # no history at all: the call refuses it
