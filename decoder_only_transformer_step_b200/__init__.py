@@ -580,6 +580,8 @@ class LogitRules:
             raise Gpt2Error(-1, f"{f}: bias_ids and bias_values belong together")
         if history is not None and history_len is None:
             raise Gpt2Error(-1, f"{f}: a history needs history_len")
+        if allowed is not None and allowed.shape[1] == 0:  # (its address is NULL: everything would be allowed)
+            raise Gpt2Error(-1, f"{f}: allowed has no words")
         self.rows = rows.pop() if rows else None
         self.tensors = {**per_row, **tables}
         width = {n: 0 if t is None else t.shape[1] for n, t in tables.items()}

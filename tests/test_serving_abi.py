@@ -279,3 +279,10 @@ def test_a_history_without_room_is_none(monkeypatch):
     r = gp.LogitRules(bias_ids=b.int(), bias_values=b)
     assert r.c.bias_values is None and r.c.n_bias == 0
     assert gp.LogitRules(append=True).c.append == 1      # no history at all: the call refuses it
+
+
+def test_a_mask_without_words_is_refused_not_taken_for_none():
+    import torch
+    for a in (torch.zeros(2, 0, dtype=torch.int32), torch.zeros(2, 8, dtype=torch.int32)[:, 3:3]):
+        with pytest.raises(gp.Gpt2Error, match="allowed has no words"):
+            gp.LogitRules(allowed=a)
