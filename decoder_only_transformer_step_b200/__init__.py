@@ -426,7 +426,7 @@ class _Torch:
         # (the bare handle of the current stream, without a Stream object around it, where this torch has it)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream_of = raw if raw is not None else lambda dev: torch.cuda.current_stream(dev).cuda_stream
-        self.current_device = torch.cuda.current_device
+        self.current_device, self.available = torch.cuda.current_device, torch.cuda.is_available
         lib = _lib()
         self.quantize, self.dequantize = lib.gpt2_op_q4_quantize, lib.gpt2_op_q4_dequantize
         self.gemv, self.prefix, self.rules = (lib.gpt2_op_gemv_q4, lib.gpt2_op_prefix_attention_bf16,
@@ -474,14 +474,19 @@ def _scratch(where, t, u8, dev):
 
 
 def _where(stream, T):
-    """(device index, stream handle) a call runs on."""
+    """(device index, stream handle) a call runs on: the current device, whose
+    kernels and limits the library takes, and the given or its current stream."""
+    try:
+        dev = T.current_device()
+    except Exception:
+        if T.available():
+            raise
+        return 0, None  # no GPU: every buffer is on another device
     if stream is None:
-        try:
-            dev = T.current_device()
-            return dev, T.stream_of(dev)
-        except Exception:  # no GPU: every buffer is on another device
-            return 0, None
-    return stream.device_index, stream.cuda_stream
+        return dev, T.stream_of(dev)
+    if stream.device_index != dev:
+        raise Gpt2Error(-1, f"the stream is on CUDA device {stream.device_index}, the current device is {dev}")
+    return dev, stream.cuda_stream
 
 
 def _extent(rows, ld, cols):

@@ -286,3 +286,21 @@ def test_a_mask_without_words_is_refused_not_taken_for_none():
     for a in (torch.zeros(2, 0, dtype=torch.int32), torch.zeros(2, 8, dtype=torch.int32)[:, 3:3]):
         with pytest.raises(gp.Gpt2Error, match="allowed has no words"):
             gp.LogitRules(allowed=a)
+
+
+def test_where_a_call_runs():
+    from types import SimpleNamespace as S
+
+    def fail():
+        raise RuntimeError("an error of the CUDA runtime")
+    T = S(current_device=lambda: 1, available=lambda: True, stream_of=lambda dev: 700 + dev)
+    assert gp._where(None, T) == (1, 701)
+    assert gp._where(S(device_index=1, cuda_stream=9), T) == (1, 9)
+    with pytest.raises(gp.Gpt2Error, match="stream is on CUDA device 0, the current device is 1"):
+        gp._where(S(device_index=0, cuda_stream=9), T)
+    # no GPU: device 0, on which no host buffer lies; with a GPU an error is not taken for that
+    assert gp._where(None, S(current_device=fail, available=lambda: False)) == (0, None)
+    with pytest.raises(RuntimeError, match="CUDA runtime"):
+        gp._where(None, S(current_device=fail, available=lambda: True))
+    with pytest.raises(RuntimeError, match="CUDA runtime"):
+        gp._where(None, S(current_device=lambda: 0, available=lambda: True, stream_of=lambda dev: fail()))
