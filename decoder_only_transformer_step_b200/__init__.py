@@ -212,6 +212,7 @@ def gpt2_create(cfg, master, shadow, grad, m, v, workspace):
                         workspace.numel() * workspace.element_size())
     ctx = ctypes.c_void_p()
     _check(_lib().gpt2_create(ctypes.byref(cfg), ctypes.byref(bufs), ctypes.byref(ctx)), "gpt2_create")
+    ctx.vocab_padded = cfg.vocab_padded  # (for the extent of logits, below)
     return ctx
 
 
@@ -627,8 +628,16 @@ def gpt2_op_logit_rules(logits, ld, out, ldo, rows, vocab, rules, next_tokens=No
 
 def gpt2_rules_next(ctx, logits, batch, rules, next_tokens, pos=None, stream=None):
     """gpt2_greedy_next under `rules` (a LogitRules); logits are rewritten in place."""
-    _check(_lib().gpt2_rules_next(ctx, _ptr(logits), batch, _rules("gpt2_rules_next", rules, batch, logits.get_device()), _ptr(next_tokens),
-                                  _ptr(pos), _stream(stream)), "gpt2_rules_next")
+    T, f = _T or _torch(), "gpt2_rules_next"
+    dev, st = _where(stream, T)
+    _check(_lib().gpt2_rules_next(ctx, _logits(f, ctx, logits, batch, T, dev), batch, _rules(f, rules, batch, dev),
+                                  _buf(f, "next_tokens", next_tokens, T.i32, dev, batch, 0),
+                                  None if pos is None else _buf(f, "pos", pos, T.i32, dev, batch, 0), st), f)
+
+
+def _logits(where, ctx, logits, batch, T, dev):
+    """Address of a batch's logits, [batch, vocab_padded] of the context's model."""
+    return _buf(where, "logits", logits, T.f32, dev, batch * getattr(ctx, "vocab_padded", 1), 0)
 
 
 def gpt2_q4_bytes(cfg: gpt2_config, group: int) -> int:
@@ -637,7 +646,9 @@ def gpt2_q4_bytes(cfg: gpt2_config, group: int) -> int:
 
 def gpt2_q4_pack(ctx, q4, group, stream=None):
     """q4: a device uint8 tensor of at least gpt2_q4_bytes(cfg, group) bytes."""
-    _check(_lib().gpt2_q4_pack(ctx, _ptr(q4), _nbytes(q4), group, _stream(stream)), "gpt2_q4_pack")
+    T, f = _T or _torch(), "gpt2_q4_pack"
+    dev, st = _where(stream, T)
+    _check(_lib().gpt2_q4_pack(ctx, _buf(f, "q4", q4, T.u8, dev, 1, 0), _nbytes(q4), group, st), f)
 
 
 def gpt2_decode_scratch_bytes(cfg: gpt2_config, batch: int, max_len: int, prefix_len: int) -> int:
@@ -645,10 +656,14 @@ def gpt2_decode_scratch_bytes(cfg: gpt2_config, batch: int, max_len: int, prefix
 
 
 def gpt2_decode_step_ex(ctx, cache, batch, max_len, tokens, pos, opts, logits, stream=None):
-    """gpt2_decode_step with a gpt2_decode_opts (or None)."""
-    _check(_lib().gpt2_decode_step_ex(ctx, _ptr(cache), _nbytes(cache), batch, max_len, _ptr(tokens), _ptr(pos),
-                                      None if opts is None else ctypes.byref(opts), _ptr(logits), _stream(stream)),
-           "gpt2_decode_step_ex")
+    """gpt2_decode_step with a gpt2_decode_opts (or None), whose addresses and sizes the caller vouches for."""
+    T, f = _T or _torch(), "gpt2_decode_step_ex"
+    dev, st = _where(stream, T)
+    _check(_lib().gpt2_decode_step_ex(ctx, _buf(f, "cache", cache, T.u8, dev, 1, 0), _nbytes(cache), batch, max_len,
+                                      _buf(f, "tokens", tokens, T.i32, dev, batch, 0),
+                                      _buf(f, "pos", pos, T.i32, dev, batch, 0),
+                                      None if opts is None else ctypes.byref(opts),
+                                      _logits(f, ctx, logits, batch, T, dev), st), f)
 
 
 # ------------------------------------------------------------ convenience ---

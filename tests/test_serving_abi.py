@@ -304,3 +304,43 @@ def test_where_a_call_runs():
         gp._where(None, S(current_device=fail, available=lambda: True))
     with pytest.raises(RuntimeError, match="CUDA runtime"):
         gp._where(None, S(current_device=lambda: 0, available=lambda: True, stream_of=lambda dev: fail()))
+
+
+def test_model_calls_refuse_short_mistyped_and_host_buffers(monkeypatch):
+    import torch
+    from types import SimpleNamespace as S
+    i32, u8 = torch.int32, torch.uint8
+    tok, pos, z = torch.zeros(3, dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(3, 128)
+    cache, none = torch.zeros(4096, dtype=u8), gp.LogitRules()
+    ctx = S(vocab_padded=128)          # what gpt2_create leaves on its context
+    with pytest.raises(gp.Gpt2Error, match="not on the current CUDA device"):
+        gp.gpt2_rules_next(ctx, z, 3, none, tok, pos)
+    with pytest.raises(gp.Gpt2Error, match="not on the current CUDA device"):
+        gp.gpt2_q4_pack(ctx, cache, 64)
+    with pytest.raises(gp.Gpt2Error, match="not on the current CUDA device"):
+        gp.gpt2_decode_step_ex(ctx, cache, 3, 4, tok, pos, None, z)
+    # host tensors pass for the current device's, and no call leaves the binding
+    calls = []
+    monkeypatch.setattr(gp, "_where", lambda *a: (-1, None))
+    lib = S(**{n: (lambda *a: calls.append(a) or 0) for n in ("gpt2_rules_next", "gpt2_q4_pack", "gpt2_decode_step_ex")},
+            gpt2_strerror=gp._lib().gpt2_strerror)
+    monkeypatch.setattr(gp, "_lib", lambda: lib)
+    step = lambda tok=tok, pos=pos, z=z, cache=cache, b=3: gp.gpt2_decode_step_ex(ctx, cache, b, 4, tok, pos, None, z)  # noqa: E731
+    nxt = lambda z=z, tok=tok, pos=pos, b=3: gp.gpt2_rules_next(ctx, z, b, none, tok, pos)  # noqa: E731
+    pack = lambda q: gp.gpt2_q4_pack(ctx, q, 64)  # noqa: E731
+    for f in (step, nxt, lambda: nxt(pos=None), lambda: pack(cache)):
+        f()
+    assert len(calls) == 4
+    short = torch.zeros(2, dtype=i32)
+    for f, what in [(lambda: step(tok=short), "tokens holds 2"), (lambda: step(pos=short), "pos holds 2"),
+                    (lambda: step(z=z[:, :127].contiguous()), "logits holds 381"), (lambda: step(b=4), "holds 3"),
+                    (lambda: step(tok=tok.long()), "tokens is torch.int64"), (lambda: step(z=z.double()), "logits is"),
+                    (lambda: step(cache=cache.float()), "cache is"), (lambda: step(z=torch.zeros(3, 256)[:, :128]), "strides"),
+                    (lambda: step(pos=None), "pos is missing"), (lambda: nxt(tok=short), "next_tokens holds 2"),
+                    (lambda: nxt(pos=short), "pos holds 2"), (lambda: nxt(z=z[:2].clone()), "logits holds 256"),
+                    (lambda: nxt(tok=tok.long()), "next_tokens is"), (lambda: nxt(z=z.half()), "logits is"),
+                    (lambda: nxt(tok=torch.zeros(6, dtype=i32)[::2]), "strides"), (lambda: pack(cache.float()), "q4 is"),
+                    (lambda: pack(cache[::2]), "strides"), (lambda: pack(cache[:0]), "q4 holds 0")]:
+        with pytest.raises(gp.Gpt2Error, match=what):
+            f()
+    assert len(calls) == 4
