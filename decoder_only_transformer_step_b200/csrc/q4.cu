@@ -1044,18 +1044,32 @@ int q4_launch_rows(Q4Args& a, const Q4Plan& p, int group, cudaStream_t st) {
   return q4_launch<2, 128>(a, p, st);
 }
 
+// Direct or streamed?  The direct kernel's time goes with its waves of blocks
+// (two blocks an SM for up to 8 rows, but one in groups of 128 that are not
+// staged) times the rounds in which a block's 16 warps walk the inputs; the
+// streamed one's, from 5 us up, with the rows x inputs that it stages.
+// Measured on both sides, in us (direct, streamed), 8 rows:
+//   4736 x 768, groups of 32 (1 wave of 1 round) 3.3, 5.5; 9472 x 768 (2 of 1) 5.6, 5.6;
+//   18944 x 128 (4 of 1) 7.8, 4.9; groups of 64, 4800 x 1664 (2 of 2) 5.4, 6.3;
+//   1600 x 8192 (1 of 8, 65536 staged) 9.0, 11.7; 16 rows, 1600 x 12288 12.5, 42;
+//   groups of 32, 1 row, 1600 x 6400 (1 of 7) 10.0, 7.5; 16 rows, 160 x 28672 34, 11.8.
+// Over 435 sizes the choice is 1.7 % above the better one on average, at most
+// 1.8 times (16 rows, 160 x 16384 in groups of 32).  Rows that are staged
+// first pay in one wave: decode step of the 350M model, batch 1, with its QKV
+// and fc products (1 wave) direct 559, streamed 602; batch 16 (2 waves of QKV)
+// 997, 949; of the 1558M model, batch 1 (QKV: 2 waves) 1892, 1576.
+bool q4_direct_pays(int rows, int N, int K, int group, bool staged) {
+  const long tiles = (N + Q4_COLS - 1) / Q4_COLS, at_once = (long)num_sms() * (rows <= 8 && (staged || group < 128) ? 2 : 1);
+  const long waves = (tiles + at_once - 1) / at_once, unit = QD_WARPS * (group < 64 ? 64 : group);
+  const long rounds = (K + unit - 1) / unit;
+  if (staged) return waves == 1 && K <= QD_STAGED_K;
+  return (waves <= 2 && waves * rounds <= 4) || (waves == 1 && K <= 16384 && (long)rows * K >= 49152);
+}
+
 int q4_run(Q4Args& a, int group, cudaStream_t st) {
-  // Few weights: the direct kernel.  Measured on both sides, in us (direct,
-  // streamed): groups of 64 and 128, N K 7.7e6 (4800 x 1600, 1 row) 4.9, 5.8,
-  // 1e7 (1600 x 6400, 8 rows) 6.0, 10.2 and 1.2e7 (16000 x 768, 16 rows) 9.7, 8.0;
-  // groups of 32, whose lanes load 4 bytes at a time, 3.7e6 (2304 x 1600, 8
-  // rows) 4.0, 5.6 and 7.7e6 (4800 x 1600, 16 rows) 10.5, 8.2.
-  const double weights = (double)a.N * a.K;
-  if (weights <= (group == 32 ? 6 << 20 : 10 << 20)) {
+  if (q4_direct_pays(a.rows, a.N, a.K, group, a.ln || a.in_f32)) {
     if (!a.ln && !a.in_f32) return a.rows <= 8 ? q4_direct<1, false>(a, group, st) : q4_direct<2, false>(a, group, st);
-    // (every block stages all rows: at 2304 x 768 a decode step of 12 layers takes 354 us, streamed 423; at
-    // 4800 x 1600 one of 48 layers 2550 us, streamed 2000)
-    if (a.K <= QD_STAGED_K && weights <= 3 << 20) return a.rows <= 8 ? q4_direct<1, true>(a, group, st) : q4_direct<2, true>(a, group, st);
+    return a.rows <= 8 ? q4_direct<1, true>(a, group, st) : q4_direct<2, true>(a, group, st);
   }
   // Rows that do not fit shared memory together: in up to three groups, each a
   // pass over the weights, else split over clusters (16 rows: 50304 x 6400 75 us

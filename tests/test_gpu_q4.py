@@ -229,7 +229,8 @@ def test_rows_of_any_magnitude_and_rows_that_are_not_finite(N, K, group, rows):
 
 
 @pytest.mark.parametrize("N,K,group", [(100, 512, 64), (130, 1280, 32), (1500, 6400, 128),     # read directly
-                                       (4200, 1536, 32), (2100, 5376, 64), (2100, 5376, 128)])  # streamed
+                                       (4200, 1536, 32), (2100, 5376, 64), (2100, 5376, 128),
+                                       (20000, 512, 32), (20000, 512, 64), (20000, 512, 128)])  # streamed
 @pytest.mark.parametrize("rows", [1, 7, 16])
 @pytest.mark.parametrize("size", [-133, -126, -100, -70, -60, 60, 100, 118, 126])
 def test_scales_of_any_magnitude(N, K, group, rows, size):
@@ -254,3 +255,17 @@ def test_scales_of_any_magnitude(N, K, group, rows, size):
     assert bool(((y.double() - want).abs() <= tol).all()), float(((y.double() - want).abs() / tol).max())
     if size >= -100:  # (the last two terms are the smallest part of it there)
         assert bool((want.abs().amax(1) > 2.0**4 * tol.amax(1)).all())
+
+
+@pytest.mark.parametrize("N,K,group", [(20000, 1536, 32), (20000, 384, 64), (20003, 1536, 128)])
+@pytest.mark.parametrize("rows", [4, 11])
+def test_streamed_rows_of_any_magnitude(N, K, group, rows):
+    test_rows_of_any_magnitude_and_rows_that_are_not_finite(N, K, group, rows)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows", [1, 8, 9, 16])
+@pytest.mark.parametrize("N,K", [(2368, 1664), (4736, 768), (4752, 768), (9472, 128), (9488, 128), (160, 4096), (160, 8192),
+                                 (90, 12288), (33, 16384)])
+def test_gemv_on_both_sides_of_the_choice_of_kernel(N, K, group, rows):
+    gemv_case(rows, N, K, group, out32=1, bias=1, seed=N + K + rows)
