@@ -22,8 +22,16 @@ constexpr int PA_ROWS = 16;      // query rows of a block (the mma M)
 constexpr int PA_BLOCKS = 444;   // blocks a call is spread over: 3 for each of 148 SMs
 template <int HD> constexpr int pa_keys() { return HD == 128 ? 16 : 32; }  // keys of a warp's step
 constexpr int PA_MIN_PART = PA_WARPS * 32;
-constexpr int PA_DIRECT_KEYS = 1024;       // a block takes all keys of its rows up to so many keys a row
-constexpr double PA_DIRECT_BYTES = 8e6;    //   and so many bytes that the whole batch reads that way
+// A block takes all keys of its rows, instead of parts that are joined, up to
+// so many keys a row (the longer a key, the fewer) and so many bytes that the
+// whole batch reads that way.  Measured on both sides, in us (all keys, parts),
+// keys of 64: 16 rows, 12 heads, 256 keys (12.6 MB) 5.4, 7.0, 512 keys (25 MB)
+// 7.15, 7.11, 768 keys 8.9, 7.6; 1 row, 12 heads, 512 keys 5.1, 5.5, 768 keys 6.1, 5.5;
+// 40 rows, 25 heads, 200 keys (51 MB) 10.6, 12.1, 256 keys (66 MB) 12.4, 11.8.
+// Keys of 128: 16 rows, 12 heads, 256 keys 8.0, 9.2, 384 keys 9.9, 9.6.  Keys of 16: 16 rows,
+// 25 heads, 512 keys 5.8, 6.5, 640 keys 6.3, 6.2.
+constexpr int pa_direct_keys(int hd) { return hd == 128 ? 256 : hd == 64 ? 512 : 640; }
+constexpr double PA_DIRECT_BYTES = 55e6;
 constexpr int PT_BLOCKS = 148;   // blocks of the tcgen05 kernel: one an SM
 // The tcgen05 kernel is taken from so many query rows of a key/value head on,
 // where their products with the prefix are so many (rows x keys x hd).
@@ -785,7 +793,7 @@ bool prefix_plan(int B, int Hq, int Hkv, int hd, int P, int max_len, PrefixPlan*
     if (L > longest + least) L = (longest + least) / least * least;
     return (int)L;
   };
-  p->direct = (long)P + max_len <= PA_DIRECT_KEYS &&
+  p->direct = (long)P + max_len <= pa_direct_keys(hd) &&
               (double)own_blocks * ((double)P + max_len) * hd * 4 <= PA_DIRECT_BYTES;
   p->tc = !p->direct && hd >= 64 && M >= PT_MIN_ROWS && (double)M * P * hd >= PT_MIN_WORK;
   if (p->tc) {

@@ -236,3 +236,14 @@ def test_maxima_that_grow_at_every_step_of_long_parts(hd, B, P, grow):
     s["pk"] = (ramp[None, :, None] * u + 0.1 * s["pk"].float()).bfloat16()
     call(s)
     check(s)
+
+
+@pytest.mark.parametrize("hd,keys", [(16, 640), (64, 512), (128, 256)])
+@pytest.mark.parametrize("over", [0, 1])
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 12, 12), (16, 25, 25), (7, 34, 2), (33, 32, 32)])
+def test_both_sides_of_the_choice_of_kernel(hd, keys, over, B, Hq, Hkv):
+    # a block for all keys of its rows up to so many keys (and 55 MB in all), parts that are joined beyond
+    m = 90
+    s = make(B, Hq, Hkv, hd, keys + over - m, m, [(b * 41) % (m + 1) for b in range(B - 1)] + [m], seed=B + hd)
+    call(s)
+    check(s)
