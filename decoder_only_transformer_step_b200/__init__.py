@@ -822,10 +822,14 @@ class KVCache:
     buffers a decode loop runs on (so the loop can be captured in a CUDA
     graph).
 
-    ``q4``: a Q4Weights whose weights the steps read.  ``prefix``: a KVCache of
+    ``q4``: a Q4Weights whose weights the steps read.  ``prefill`` has no 4-bit
+    form and computes the prompt with the model's own weights, so that keys,
+    values and the first choice are those of the unrounded model; a prompt fed
+    by ``step`` sees the 4-bit weights throughout.  ``prefix``: a KVCache of
     one sequence, already filled, whose first ``prefix_len`` positions precede
     every row's own (``prefix_len + max_len <= n_ctx``); the rows' own tokens,
-    prompts included, are then fed by ``step``."""
+    prompts included, are then fed by ``step``, with ``pos += 1`` after each
+    but the last, which ``greedy_advance`` follows."""
 
     def __init__(self, model: "GPT2", batch: int, max_len: int, prefix: "KVCache" = None, prefix_len: int = 0,
                  q4: Q4Weights = None):
@@ -862,7 +866,8 @@ class KVCache:
     def prefill(self, tokens, prompt_len):
         """tokens: int32 [batch, n_ctx] (device); prompt_len: int32 [batch]
         (device).  Leaves the logits after each prompt in self.logits, the
-        greedy next id in self.tokens and self.pos = prompt_len."""
+        greedy next id in self.tokens and self.pos = prompt_len.  Reads the
+        model's own weights, with q4 too."""
         if self.opts_prefix:
             raise ValueError("rows behind a prefix are fed by step(): prefill would not see the prefix")
         gpt2_prefill(self.model.ctx, self.buf, self.batch, self.max_len, tokens, prompt_len, self.logits)
@@ -872,7 +877,7 @@ class KVCache:
 
     def step(self, tokens=None, pos=None):
         """One decode step on self.tokens / self.pos (or the given device
-        tensors); returns the logits [batch, vocab_padded]."""
+        tensors); returns the logits [batch, vocab_padded].  self.pos stays."""
         tokens, pos = self.tokens if tokens is None else tokens, self.pos if pos is None else pos
         if self.opts is None:
             gpt2_decode_step(self.model.ctx, self.buf, self.batch, self.max_len, tokens, pos, self.logits)

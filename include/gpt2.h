@@ -306,7 +306,8 @@ int gpt2_q4_pack(gpt2_ctx* ctx, void* q4, size_t q4_bytes, int group, void* stre
 
 /* Options of gpt2_decode_step_ex; a zeroed struct asks for nothing. */
 typedef struct {
-  const void* q4;         /* 4-bit weights (gpt2_q4_pack) in place of the shadow's, or NULL */
+  const void* q4;         /* 4-bit weights (gpt2_q4_pack) in place of the shadow's, or NULL; gpt2_prefill */
+                          /*   has no such form, its keys and values are those of the shadow's weights */
   size_t q4_bytes;
   int q4_group;
   const void* prefix;     /* a cache of one sequence, sized for (1, prefix_cap), whose first prefix_len */

@@ -217,3 +217,49 @@ def test_refusals_of_the_model_calls():
     c.pos.fill_(10)
     c.step()
     assert model.status() == bad["GPT2_ERR_POSITION_RANGE"]
+
+
+def test_prompts_fed_by_steps_behind_a_prefix_as_documented():
+    # step, pos += 1, ..., step, greedy_advance: the rows end where a prefill of their whole sequences ends
+    oc, batch, P, n = TINY, 3, 21, 6
+    model, _ = make_model(oc, 1)
+    whole, _ = inputs.uniform_tokens(batch, oc.n_ctx, oc.vocab - 12, seed=75)
+    whole[:, :P] = whole[0, :P]
+    plain = gp.KVCache(model, batch, P + 20)
+    plain.prefill(i32(whole), i32([P + n] * batch))
+    first = plain.logits[:, : oc.vocab - 12].clone()
+    pre = gp.KVCache(model, 1, P)
+    pre.prefill(i32(whole[:1]), i32([P]))
+    cache = gp.KVCache(model, batch, 20, prefix=pre, prefix_len=P)
+    hist = torch.full((batch, 16), -1, dtype=torch.int32, device="cuda")
+    length = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    rules = gp.LogitRules(history=hist, history_len=length, append=True)
+    prompt = i32(whole[:, P:P + n])
+    for i in range(n):
+        cache.step(prompt[:, i].contiguous())
+        if i + 1 < n:
+            cache.pos += 1
+    z = cache.logits[:, : oc.vocab - 12].clone()
+    assert float((z - first).abs().max()) <= 1e-4 * float(first.abs().max())      # the fp32 mode's tolerance
+    cache.greedy_advance(rules)
+    assert cache.pos.tolist() == [n] * batch and length.tolist() == [1] * batch   # the prompt is nobody's choice
+    for _ in range(5):
+        cache.step()
+        cache.greedy_advance(rules)
+        plain.step()
+        plain.greedy_advance()
+        assert float((cache.logits - plain.logits)[:, : oc.vocab - 12].abs().max()) <= 2e-4 * float(first.abs().max())
+        assert torch.equal(cache.tokens, plain.tokens)
+    assert cache.pos.tolist() == [n + 5] * batch and hist[:, :6].tolist() == hist[:, :6].clamp(0).tolist()
+    assert model.status() == 0
+
+
+def test_prefill_beside_4_bit_weights_is_that_of_the_models_own():
+    oc = HD64
+    model, _ = make_model(oc, 0)
+    tok, lens = i32(inputs.uniform_tokens(2, oc.n_ctx, oc.vocab - 12, seed=76)[0]), i32([9, 30])
+    a, b = gp.KVCache(model, 2, 40), gp.KVCache(model, 2, 40, q4=gp.Q4Weights(model, 64))
+    a.prefill(tok, lens)
+    b.prefill(tok, lens)
+    assert torch.equal(a.logits, b.logits) and torch.equal(a.tokens, b.tokens)
+    assert not torch.equal(a.step(), b.step())
