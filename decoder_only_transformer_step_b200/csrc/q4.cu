@@ -233,7 +233,9 @@ __global__ void __launch_bounds__(256)
 // scales) into a ring of its own with cp.async, several ahead, across tile
 // borders: no block-wide wait stands in the stream.  Inputs too long for
 // shared memory are split over the blocks of a cluster (up to 8), whose sums
-// meet through distributed shared memory, again in a fixed order.
+// meet through distributed shared memory, again in a fixed order (the rows in
+// two or three groups, each a pass over the weights, instead: groups of 128, 16
+// x 50304 x 6400 75 us, split 71; 5 x 28673 x 16384 110, 60).
 //
 // 8 x 50304 x 1600, groups of 32: 18 us (2.6 TB/s); 5 x 28673 x 8192, groups of
 // 128: 33 us (3.6 TB/s, 27.6 without the products): half the issue slots and
@@ -954,7 +956,7 @@ struct Q4Plan {
   int split, kr, ks, ring, part, grid;
   size_t smem;
 };
-bool q4_plan(int rows, int N, int K, int group, bool ln, Q4Plan* p) {
+bool q4_plan(int rows, int N, int K, int group, Q4Plan* p) {
   const int NR = rows <= 8 ? 8 : 16;
   const int slot = q4_slot(group);
   const int nst = (K + Q4_STAGE - 1) / Q4_STAGE, ntiles = (N + Q4_COLS - 1) / Q4_COLS;
@@ -1049,11 +1051,11 @@ int q4_launch_rows(Q4Args& a, const Q4Plan& p, int group, cudaStream_t st) {
 // staged) times the rounds in which a block's 16 warps walk the inputs; the
 // streamed one's, from 5 us up, with the rows x inputs that it stages.
 // Measured on both sides, in us (direct, streamed), 8 rows:
-//   4736 x 768, groups of 32 (1 wave of 1 round) 3.3, 5.5; 9472 x 768 (2 of 1) 5.6, 5.6;
+//   4736 x 768, groups of 32 (1 wave of 1 round) 3.3, 5.3; 9472 x 768 (2 of 1) 5.6, 5.6;
 //   18944 x 128 (4 of 1) 7.8, 4.9; groups of 64, 4800 x 1664 (2 of 2) 5.4, 6.3;
-//   1600 x 8192 (1 of 8, 65536 staged) 9.0, 11.7; 16 rows, 1600 x 12288 12.5, 42;
+//   1600 x 8192 (1 of 8, 65536 staged) 9.0, 11.8; 16 rows, 1600 x 12288 12.6, 24;
 //   groups of 32, 1 row, 1600 x 6400 (1 of 7) 10.0, 7.5; 16 rows, 160 x 28672 34, 11.8.
-// Over 435 sizes the choice is 1.7 % above the better one on average, at most
+// Over 435 sizes the choice is 2.1 % above the better one on average, at most
 // 1.8 times (16 rows, 160 x 16384 in groups of 32).  Rows that are staged
 // first pay in one wave: decode step of the 350M model, batch 1, with its QKV
 // and fc products (1 wave) direct 559, streamed 602; batch 16 (2 waves of QKV)
@@ -1071,26 +1073,8 @@ int q4_run(Q4Args& a, int group, cudaStream_t st) {
     if (!a.ln && !a.in_f32) return a.rows <= 8 ? q4_direct<1, false>(a, group, st) : q4_direct<2, false>(a, group, st);
     return a.rows <= 8 ? q4_direct<1, true>(a, group, st) : q4_direct<2, true>(a, group, st);
   }
-  // Rows that do not fit shared memory together: in up to three groups, each a
-  // pass over the weights, else split over clusters (16 rows: 50304 x 6400 75 us
-  // in two passes, 185 us over clusters; 8 rows, 8192 x 28672 145 us in four).
   Q4Plan p;
-  for (int groups = 1; groups <= (a.ln ? 1 : 3); ++groups) {
-    const int per = (a.rows + groups - 1) / groups;
-    if (!q4_plan(per, a.N, a.K, group, a.ln != 0, &p) || (p.split > 1 && !a.ln)) continue;
-    const int rows = a.rows;
-    for (int r0 = 0; r0 < rows; r0 += per) {
-      Q4Args b = a;
-      b.rows = rows - r0 < per ? rows - r0 : per;
-      b.in = reinterpret_cast<const uint8_t*>(a.in) + (size_t)r0 * a.ldi * (a.in_f32 || a.ln ? 4 : 2);
-      b.out = reinterpret_cast<uint8_t*>(a.out) + (size_t)r0 * a.ldo * (a.epi == Q4_BF16 || a.epi == Q4_GELU ? 2 : 4);
-      if (!q4_plan(b.rows, a.N, a.K, group, a.ln != 0, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
-      const int rc = q4_launch_rows(b, p, group, st);
-      if (rc != GPT2_OK) return rc;
-    }
-    return GPT2_OK;
-  }
-  if (!q4_plan(a.rows, a.N, a.K, group, a.ln != 0, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
+  if (!q4_plan(a.rows, a.N, a.K, group, &p)) return GPT2_ERR_UNSUPPORTED_SHAPE;
   return q4_launch_rows(a, p, group, st);
 }
 
