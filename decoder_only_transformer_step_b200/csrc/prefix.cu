@@ -4,9 +4,10 @@
 //   z[j] = q . k[j] / sqrt(hd),  j over the P prefix keys and the row's own
 //   o = sum_j exp(z[j] - lse) v[j],  lse = log sum_j exp(z[j])
 //
-// The prefix is read once for all rows: the query rows of a key/value head
-// (batch x heads that share it) are the rows of one matrix product per block
-// of keys, instead of B passes over the same keys.  Work is split along the
+// The query rows of a key/value head (batch x heads that share it) are the rows
+// of one matrix product per block of keys, instead of B passes over the same
+// keys: the prefix is read once for every 16 of them, or for up to 256 on
+// tcgen05; only where it is short does each sequence read it for itself.  Work is split along the
 // keys into parts of a fixed length; a part leaves, per row, its running
 // maximum, sum and weighted values (fp32), and a second kernel joins a row's
 // parts in a fixed order.  Rows without any key get o = 0, lse = -inf.

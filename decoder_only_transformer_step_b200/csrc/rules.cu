@@ -48,7 +48,7 @@ struct RulesArgs {
 // take their path for one lane.  384 x 50257 with histories of 4096 ids: 63 us
 // (logits in and out at 2.5 TB/s, issue slots 65 % busy), 42 without a history,
 // 36 without biases too, 27 without mask and choice as well; 16 x 50257: 7.2 us, one
-// round trip after the other.
+// round trip after the other: lengths and history, mask, listed ids, exchange.
 template <bool COUNTED, bool MASKED>
 __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_constant__ RulesArgs a) {
   extern __shared__ __align__(16) uint32_t rl_word[];  // [per] words, [n_bias] bias values, [list] ids
@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(RL_THREADS) logit_rules_kernel(const __grid_co
     for (int i = tid; i < a.per / 4; i += RL_THREADS) reinterpret_cast<uint4*>(rl_word)[i] = make_uint4(0, 0, 0, 0);
   }
   pdl_wait();
-  // every first load is requested here, so that the phases below wait for HBM
-  // once: the row's lengths, its first history and bias entry, its logits
+  // requested here, ahead of the phases below: the row's lengths, its first
+  // history and bias entries, its first logits (the mask's words and the
+  // penalties are requested where they are used, the listed ids' logits again)
   int hn = 0, g0 = 0, be = -1, h0[UH];
   float bval = 0.f;
   const size_t brow = (size_t)row * a.n_bias;

@@ -327,8 +327,9 @@ size_t gpt2_decode_scratch_bytes(const gpt2_config* cfg, int batch, int max_len,
  * and attends to the prefix and to the row's own positions 0..pos[b]; the
  * prefix cache is only read, so several batches may share it, and a row's
  * own cache holds nothing of it.  pos[b] still counts the row's own
- * positions (0 <= pos[b] < max_len).  In modes 0 and 2 the queries and the
- * attention's output are then rounded to bf16, as in the forward.  Steps in
+ * positions (0 <= pos[b] < max_len).  In modes 0 and 2 the queries, the
+ * probabilities and the attention's output are then rounded to bf16, as in the
+ * forward (without a prefix the step holds the first two in fp32).  Steps in
  * flight at the same time need scratch of their own, captured graphs among
  * them. */
 int gpt2_decode_step_ex(gpt2_ctx* ctx, void* cache, size_t cache_bytes, int batch, int max_len,
@@ -539,15 +540,17 @@ int gpt2_op_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int N, 
  * depends on the sizes only; where the weights are streamed (many of them) as
  * sum (q + 8) x - 8 sum x, group by group.  x may have any magnitude.  Scales
  * below 2^-100 lose: there an addition may be off by 2^-131 of the row's largest
- * |x|.  K at most 32768.  Errors as above; rows > 16 is INVALID_ARG. */
+ * |x|.  An infinity or NaN in a row of x or in a scale makes the sums that it
+ * enters infinite or NaN, which of the two depends on the kernel.  K at most
+ * 32768.  Errors as above; rows > 16 is INVALID_ARG. */
 int gpt2_op_gemv_q4(const uint16_t* x, int ldx, const uint8_t* packed, const uint16_t* scales, const uint16_t* bias,
                     void* out, int out_fp32, int ldo, int rows, int N, int K, int group, void* stream);
 
 /* ---- attention over a shared prefix ----------------------------------------
  * One new token per sequence: query head h of row b attends to the
  * prefix_len keys of its key/value head h / (Hq / Hkv) in the prefix, which
- * is the same for all rows and read once, and to the first len[b] keys of the
- * row's own cache:
+ * is the same for all rows (and read once for many of them, not by each), and
+ * to the first len[b] keys of the row's own cache:
  *   o[b, h] = softmax(q . k / sqrt(hd)) v,  lse[b, h] = log sum exp(q . k / sqrt(hd))
  * q, o bf16 [B, Hq * hd] with row pitches ldq, ldo (even, 4-byte aligned);
  * pk, pv bf16 [Hkv][prefix_cap][hd]; k, v bf16 [B][Hkv][max_len][hd] (16-byte
@@ -557,7 +560,9 @@ int gpt2_op_gemv_q4(const uint16_t* x, int ldx, const uint8_t* packed, const uin
  * part's pointers may be NULL.  A row without any key gets o = 0, lse = -inf.
  * Keys past prefix_len or len[b] are not read.  scratch: device, 16-byte
  * aligned, at least the given bytes (0 for invalid sizes); calls in flight at
- * the same time need scratch of their own.  Sums are in a fixed order. */
+ * the same time need scratch of their own.  Sums are fp32 in a fixed order; for
+ * the product with v the probabilities are rounded to bf16 (by 2^-8 of each at
+ * most), their sum and lse are formed of the unrounded ones. */
 size_t gpt2_op_prefix_attention_scratch_bytes(int B, int Hq, int Hkv, int hd, int prefix_len, int max_len);
 int gpt2_op_prefix_attention_bf16(const uint16_t* q, int ldq, const uint16_t* pk, const uint16_t* pv, int prefix_len,
                                   int prefix_cap, const uint16_t* k, const uint16_t* v, const int32_t* len, int max_len,
@@ -566,7 +571,8 @@ int gpt2_op_prefix_attention_bf16(const uint16_t* q, int ldq, const uint16_t* pk
 
 /* Rules on logits (see gpt2_logit_rules) for any number of rows: out[r, v] for
  * v < vocab from logits[r, v] (fp32, row pitches ldo and ld; the same buffer
- * and pitch for an update in place; columns past vocab are left as they were),
+ * and pitch for an update in place, else buffers that do not overlap; columns
+ * past vocab are left as they were),
  * next[r] (NULL: none) the greedy choice as gpt2_rules_next, pos[r] += 1 (NULL:
  * none; only with next).  vocab at most 262144. */
 int gpt2_op_logit_rules(const float* logits, int ld, float* out, int ldo, int rows, int vocab,
