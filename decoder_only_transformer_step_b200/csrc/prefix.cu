@@ -112,7 +112,10 @@ template <int HD> constexpr int pa_smem() {
 // ahead) without block-wide waits, with its own running maximum and sum; the
 // warps meet once at the end.  Probabilities are rounded to bf16 for the
 // second product (its operand type; their sum stays fp32 of the unrounded
-// ones): half a step, 2^-8 relative at most, as the output's own rounding.
+// ones): half a step, 2^-8 relative at most, as the output's own rounding, and
+// 1.1 times the error of a bf16 output of unrounded ones.  (A second product
+// with what the rounding leaves costs 6 to 15 %: 16 x 12 x 3500 9.7 -> 10.3 us, 1 x
+// 12 x 400 5.0 -> 5.8.)
 // Where a row has few keys in all and the whole batch reads little (DIRECT), a
 // block takes all keys of its rows instead, those of the prefix and then their
 // own, and writes the output itself: 3 rows, 12 heads, 200 + 64 keys of 64 in

@@ -537,7 +537,7 @@ int gpt2_op_q4_dequantize(const uint8_t* packed, const uint16_t* scales, int N, 
  * rows, the linear layer of a decode step.  x bf16 [rows, ldx] (ldx a multiple
  * of 8, 16-byte aligned), bias bf16 [N] or NULL, out bf16 or fp32 [rows, ldo],
  * any N and ldo >= N.  Products are exact and summed in fp32, in an order that
- * depends on the sizes only; where the weights are streamed (many of them) as
+ * depends on the sizes only; where the weights are streamed through shared memory as
  * sum (q + 8) x - 8 sum x, group by group.  x may have any magnitude.  Scales
  * below 2^-100 lose: there an addition may be off by 2^-131 of the row's largest
  * |x|.  An infinity or NaN in a row of x or in a scale makes the sums that it
